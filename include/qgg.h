@@ -368,6 +368,128 @@ qgg_status moe_router_bwd(const qgg_qweight* w_gate_up, const qgg_qweight* w_dow
                           int inter, int variant, int chunk, void* workspace, size_t ws_bytes,
                           uint16_t* dx, float* dgates, float* dlogits, qgg_stream_t stream);
 
+/* ---- Scored routing ------------------------------------------------------
+ * Routers that score experts by a softmax or a sigmoid, balance their load by
+ * a bias that enters the choice only, and choose among groups of experts. */
+#define QGG_SCORE_SOFTMAX 0
+#define QGG_SCORE_SIGMOID 1
+
+#define QGG_F32 0             /* element type of the router's logits */
+#define QGG_BF16 1
+
+/* score       QGG_SCORE_*
+ * n_group     equal groups of consecutive experts (divides E); 1 = no groups
+ * topk_group  groups an expert may be chosen from; n_group = all of them
+ * group_top   a group's score is the sum of its 1 or 2 largest choice values
+ * renorm      nonzero: the kept scores are divided by their sum
+ * scale       factor on the gates */
+typedef struct {
+  int32_t score;
+  int32_t n_group, topk_group, group_top;
+  int32_t renorm;
+  float scale;
+} qgg_route_opts;
+
+/* moe_route_scored -- per token, with logits l [T][E] (fp32 or BF16 by
+ * logits_type): s = softmax(l) over all E, or 1 / (1 + exp(-l)); choice values
+ * c = s + bias (bias [E] fp32, may be NULL); the topk_group best groups by
+ * the sum of their group_top largest c (ties: the lower group); in them the k
+ * experts with the largest c (ties: the lower id).  topk_ids [T][k] in that
+ * order, topk_gates [T][k] = scale * s[id], divided by the kept scores' sum
+ * when renorm is set (0 where that sum is 0).  Scores and choice values are
+ * formed in 64 bits, gates rounded once to fp32.  A logit that is not finite
+ * has score 0 and comes after every finite one; a bias entry that is not
+ * finite puts its expert there too; both set *err_flag (bit 1).
+ * Limits as moe_route, and topk_group * (E / n_group) >= k, group_top <= E /
+ * n_group (QGG_ERR_INVALID_ARG); n_group <= 64 when topk_group < n_group
+ * (QGG_ERR_UNSUPPORTED). */
+qgg_status moe_route_scored(const void* logits, int logits_type, const float* bias, int T, int E,
+                            int k, const qgg_route_opts* opts, int32_t* topk_ids,
+                            float* topk_gates, int32_t* err_flag, qgg_stream_t stream);
+
+/* moe_route_scored_bwd -- dlogits [T][E] (the logits' type, every entry
+ * written) from dgates [T][k] with the choice topk_ids held fixed; opts'
+ * score, renorm and scale as in the forward (the group fields are not read,
+ * the bias has no gradient).  Experts not kept get 0, except under a softmax
+ * without renorm, whose gradient reaches every expert.  An id that occurs
+ * twice in a row gets the sum; ids outside [0, E) and experts whose logit is
+ * not finite contribute nothing. */
+qgg_status moe_route_scored_bwd(const void* logits, int logits_type, const int32_t* topk_ids,
+                                const float* dgates, int T, int E, int k,
+                                const qgg_route_opts* opts, void* dlogits, qgg_stream_t stream);
+
+/* ---- 8-bit floating point --------------------------------------------------
+ * Rows: OCP E4M3 codes [rows][cols] with one E8M0 scale byte per 128 columns,
+ * [rows][ceil(cols / 128)] (value 2^(c - 127), 255 = NaN; a last block may be
+ * shorter).  The scale of a block is 2^e with e the least integer >= -127
+ * such that max |x| <= 448 * 2^e (e = 0 for a block of zeros); a code is
+ * x / 2^e rounded to nearest even.  A value that is not finite becomes the
+ * NaN code and does not count for its block's scale. */
+/* qgg_fp8_quantize -- BF16 rows to codes and scales; cols % 8 == 0. */
+qgg_status qgg_fp8_quantize(const uint16_t* x, int64_t rows, int cols, uint8_t* codes,
+                            uint8_t* scales, qgg_stream_t stream);
+/* qgg_fp8_dequantize -- codes and scales back to BF16 (code * scale, rounded
+ * once; exact unless the product falls below BF16's normal range). */
+qgg_status qgg_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                              uint16_t* x, qgg_stream_t stream);
+
+#define QGG_SCALE_E8M0 0
+#define QGG_SCALE_F32 1
+/* Frozen 8-bit expert weights, [E][N][K] E4M3 codes with one scale per 128 x
+ * 128 block, [E][ceil(N / 128)][K / 128] (uint8 E8M0 or fp32 by scale_type). */
+typedef struct {
+  int32_t E, N, K;
+  int32_t scale_type;
+  const uint8_t* codes;
+  const void* scales;
+} qgg_fp8_weight;
+
+/* fp8_grouped_gemm -- dequant_grouped_gemm for 8-bit weights and activations:
+ * y[i][:] = a_row(i) . W_e^T for every sorted row i of expert e, or, with
+ * QGG_TRANSPOSE_W, a_row(i) . W_e (a then has N columns and y [P][K]).
+ * a, a_scales are rows in the format above (K or N columns), T of them with
+ * QGG_A_TOKENS, else P; products and sums in fp32, y BF16 in sorted order.
+ * Rows of y at and past offsets[E] are left as they are.  The call needs no
+ * workspace, so calls on different streams need nothing of their own.
+ * K % 128 == 0, N % 64 == 0, the reduced width at most 32768, N * K and a's
+ * bytes below 2^32 - 16, else QGG_ERR_UNSUPPORTED; codes, a and y 16-byte
+ * aligned.  Deterministic. */
+qgg_status fp8_grouped_gemm(const qgg_fp8_weight* w, const uint8_t* a, const uint8_t* a_scales,
+                            int flags, const qgg_perm* p, int T, int k, uint16_t* y,
+                            qgg_stream_t stream);
+
+/* moe_swiglu_fp8 -- a = silu(h[:, :inter]) * h[:, inter:] of P routed rows h
+ * [P][2 inter] BF16, in fp32, rounded once: a [P][inter] BF16 (for 4-bit down
+ * projections) and / or a8, a8_scales in the 8-bit row format (for
+ * fp8_grouped_gemm); and the rows' 8-bit activation checkpoint h8 [P][2
+ * inter], h8_scales [P][2 inter / 128] for moe_swiglu_fp8_bwd.  Each output is
+ * nullable (a8 / h8 with their scales; at least one given).  n_rows (device,
+ * nullable; offsets + E of the permutation): rows at and past *n_rows are
+ * neither read nor written.  inter % 128 == 0. */
+qgg_status moe_swiglu_fp8(const uint16_t* h, const int32_t* n_rows, int64_t P, int inter,
+                          uint16_t* a, uint8_t* a8, uint8_t* a8_scales, uint8_t* h8,
+                          uint8_t* h8_scales, qgg_stream_t stream);
+
+/* moe_swiglu_fp8_bwd -- from the checkpoint: with gate | up the values of h8,
+ * da [P][inter] BF16 the gradient of a before the gate (dY[t] . W_down), g
+ * the pair's gate: dh = [g da up silu'(gate) | g da silu(gate)] as BF16
+ * [P][2 inter] and / or dh8, dh8_scales in the 8-bit row format; dgates
+ * [T][k] fp32 = <da, silu(gate) up> per pair (0 for a pair the permutation
+ * dropped).  Each output nullable (dh8 with its scales; at least one given).
+ * Rows of dh at and past offsets[E] are left as they are.  inter % 128 == 0.
+ * Deterministic. */
+qgg_status moe_swiglu_fp8_bwd(const uint16_t* da, const uint8_t* h8, const uint8_t* h8_scales,
+                              const float* topk_gates, const qgg_perm* p, int T, int k, int inter,
+                              uint16_t* dh, uint8_t* dh8, uint8_t* dh8_scales, float* dgates,
+                              qgg_stream_t stream);
+
+/* moe_combine -- y[t] = sum_j g[t, j] rows[inv_perm[t k + j]] over the sorted
+ * rows [P][d] BF16 (the last step of moe_ffn_fwd; gates NULL: plain sum, the
+ * last step of moe_dx_bwd), fp32 in ascending j, y [T][d] BF16.  Dropped
+ * pairs add nothing.  d % 8 == 0. */
+qgg_status moe_combine(const uint16_t* rows, int d, const qgg_perm* p, const float* topk_gates,
+                       int T, int k, uint16_t* y, qgg_stream_t stream);
+
 /* qgg_repack_weights -- copy a QGG_LAYOUT_ROWS weight tensor into the
  * QGG_LAYOUT_MFMA order: packed_out gets E*N*K/2 bytes, scales_out E*N*K/32
  * scale entries (device buffers the caller owns, not aliasing the source).

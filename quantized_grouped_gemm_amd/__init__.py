@@ -7,7 +7,9 @@ library is not built, every call raises; there is no fallback.
 
 Names follow the C-ABI in ``include/qgg.h``: ``moe_route``, ``expert_permute``,
 ``dequant_grouped_gemm``, ``lora_grouped_gemm``, ``moe_ffn_fwd``, ``moe_dx_bwd``,
-``moe_router_bwd``.
+``moe_router_bwd``; scored routing (``moe_route_scored``, ``moe_route_scored_bwd``) and 8-bit
+floating point (``fp8_quantize``, ``fp8_dequantize``, ``fp8_grouped_gemm``, ``swiglu_fp8``,
+``swiglu_fp8_bwd``, ``moe_combine``).
 """
 from __future__ import annotations
 
@@ -43,7 +45,9 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too sm
 EXPORTS = ("moe_route", "expert_permute", "dequant_grouped_gemm", "lora_grouped_gemm",
            "lora_grouped_gemm_bwd", "moe_ffn_fwd", "moe_ffn_fwd_noalloc", "moe_ffn_fwd_lora",
            "moe_dx_bwd", "moe_ffn_bwd_lora",
-           "moe_router_bwd", "qgg_repack_weights", "qgg_check_weights", "qgg_workspace_bytes",
+           "moe_router_bwd", "moe_route_scored", "moe_route_scored_bwd", "qgg_fp8_quantize",
+           "qgg_fp8_dequantize", "fp8_grouped_gemm", "moe_swiglu_fp8", "moe_swiglu_fp8_bwd",
+           "moe_combine", "qgg_repack_weights", "qgg_check_weights", "qgg_workspace_bytes",
            "qgg_set_timing_events", "qgg_timing_count", "qgg_timing_kind", "qgg_status_string",
            "qgg_version")
 
@@ -63,6 +67,18 @@ class _QWeight(ctypes.Structure):
 class _Lora(ctypes.Structure):
     _fields_ = [("rank", ctypes.c_int32), ("alpha", ctypes.c_float), ("A", ctypes.c_void_p),
                 ("B", ctypes.c_void_p)]
+
+
+class _RouteOpts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _Fp8Weight(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("scale_type", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 class _Perm(ctypes.Structure):
@@ -122,6 +138,23 @@ def lib():
         L.qgg_status_string.argtypes = [i32]
         L.qgg_status_string.restype = ctypes.c_char_p
         L.qgg_version.restype = ctypes.c_char_p
+        i64 = ctypes.c_int64
+        L.moe_route_scored.argtypes = [P, i32, P, i32, i32, i32, ctypes.POINTER(_RouteOpts), P, P,
+                                       P, P]
+        L.moe_route_scored_bwd.argtypes = [P, i32, P, P, i32, i32, i32,
+                                           ctypes.POINTER(_RouteOpts), P, P]
+        L.qgg_fp8_quantize.argtypes = [P, i64, i32, P, P, P]
+        L.qgg_fp8_dequantize.argtypes = [P, P, i64, i32, P, P]
+        L.fp8_grouped_gemm.argtypes = [ctypes.POINTER(_Fp8Weight), P, P, i32,
+                                       ctypes.POINTER(_Perm), i32, i32, P, P]
+        L.moe_swiglu_fp8.argtypes = [P, P, i64, i32, P, P, P, P, P, P]
+        L.moe_swiglu_fp8_bwd.argtypes = [P, P, P, P, ctypes.POINTER(_Perm), i32, i32, i32, P, P, P,
+                                         P, P]
+        L.moe_combine.argtypes = [P, i32, ctypes.POINTER(_Perm), P, i32, i32, P, P]
+        for f in ("moe_route_scored", "moe_route_scored_bwd", "qgg_fp8_quantize",
+                  "qgg_fp8_dequantize", "fp8_grouped_gemm", "moe_swiglu_fp8", "moe_swiglu_fp8_bwd",
+                  "moe_combine"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("moe_route", "expert_permute", "dequant_grouped_gemm", "lora_grouped_gemm",
                   "lora_grouped_gemm_bwd", "moe_ffn_fwd", "moe_ffn_fwd_noalloc",
                   "moe_ffn_fwd_lora", "moe_dx_bwd", "moe_ffn_bwd_lora", "moe_router_bwd"):
@@ -551,3 +584,288 @@ def moe_router_bwd(w_gate_up: QWeight, w_down: QWeight, dy, topk_ids, topk_gates
                                 inter, variant, chunk, _ptr(buf), buf.numel(), _ptr(dx), _ptr(dg),
                                 _ptr(dl), _stream()), "moe_router_bwd")
     return {"dx": dx, "dgates": dg, "dlogits": dl}
+
+
+# ---- scored routing and 8-bit floating point -------------------------------
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+SCALE_BLOCK = 128          # columns of a row, or rows and columns of a weight, per scale
+
+
+def _need(name: str, t, dtypes, shape=None, device=None):
+    """Raise unless t is a contiguous CUDA tensor of one of the dtypes, of the shape (-1: any)
+    and on the device."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise QggError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise QggError(f"{name}: dtype {t.dtype}, want {' or '.join(map(str, dtypes))}")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(w not in (-1, n) for n, w in zip(t.shape, shape))):
+        raise QggError(f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
+    if not t.is_cuda:
+        raise QggError(f"{name}: on {t.device}, want a GPU")
+    if device is not None and t.device != device:
+        raise QggError(f"{name}: on {t.device}, the call's other tensors are on {device}")
+    if not t.is_contiguous():
+        raise QggError(f"{name}: not contiguous")
+
+
+class _On:
+    """Makes a tensor's device current for a call (launches go to the current device)."""
+
+    def __init__(self, device):
+        import torch
+        self.guard = None
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _need_perm(perm: Perm, P: int, device, E: int | None = None):
+    import torch
+    i32 = (torch.int32,)
+    if E is None:
+        E = perm.counts.numel()
+    for name, n in (("counts", E), ("offsets", E + 1), ("active", E), ("n_active", 1),
+                    ("perm", P), ("inv_perm", P)):
+        t = getattr(perm, name)
+        _need(f"perm.{name}", t, i32, None, device)
+        if t.numel() != max(n, 1):
+            raise QggError(f"perm.{name}: {t.numel()} entries, want {max(n, 1)}")
+
+
+def _code_types():
+    import torch
+    return (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _route_opts(score, n_group, topk_group, group_top, renorm, scale):
+    if score not in SCORES:
+        raise QggError(f"score {score!r}, want one of {sorted(SCORES)}")
+    return _RouteOpts(SCORES[score], n_group, topk_group, group_top, int(bool(renorm)),
+                      float(scale))
+
+
+def moe_route_scored(logits, k: int, score: str = "sigmoid", bias=None, n_group: int = 1,
+                     topk_group: int = 1, group_top: int = 2, renorm: bool = True,
+                     scale: float = 1.0, err_flag=None):
+    """(topk_ids int32 [T,k], topk_gates fp32 [T,k]) for fp32 or BF16 logits [T,E]: softmax or
+    sigmoid scores, `bias` [E] fp32 added for the choice only, the `topk_group` best of
+    `n_group` groups by the sum of their `group_top` best, gates renormalised and scaled."""
+    import torch
+    _need("logits", logits, (torch.float32, torch.bfloat16), (-1, -1))
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _need("bias", bias, (torch.float32,), (E,), dev)
+    if err_flag is not None:
+        _need("err_flag", err_flag, (torch.int32,), (1,), dev)
+    if n_group == 1:
+        group_top = 1
+    o = _route_opts(score, n_group, topk_group, group_top, renorm, scale)
+    with _On(dev):
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        gates = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+        _check(lib().moe_route_scored(_ptr(logits), int(logits.dtype == torch.bfloat16),
+                                      _ptr(bias), T, E, k, ctypes.byref(o), _ptr(ids), _ptr(gates),
+                                      _ptr(err_flag), _stream()), "moe_route_scored")
+    return ids, gates
+
+
+def moe_route_scored_bwd(logits, topk_ids, dgates, score: str = "sigmoid", renorm: bool = True,
+                         scale: float = 1.0):
+    """dlogits [T,E] (the logits' dtype) from dgates fp32 [T,k], the choice topk_ids held fixed."""
+    import torch
+    _need("logits", logits, (torch.float32, torch.bfloat16), (-1, -1))
+    T, E = logits.shape
+    dev = logits.device
+    _need("topk_ids", topk_ids, (torch.int32,), (T, -1), dev)
+    k = topk_ids.shape[1]
+    _need("dgates", dgates, (torch.float32,), (T, k), dev)
+    o = _route_opts(score, 1, 1, 1, renorm, scale)
+    with _On(dev):
+        dl = torch.empty_like(logits)
+        _check(lib().moe_route_scored_bwd(_ptr(logits), int(logits.dtype == torch.bfloat16),
+                                          _ptr(topk_ids), _ptr(dgates), T, E, k, ctypes.byref(o),
+                                          _ptr(dl), _stream()), "moe_route_scored_bwd")
+    return dl
+
+
+def fp8_quantize(x):
+    """(codes float8_e4m3fn [M,C], scales float8_e8m0fnu [M,ceil(C/128)]) of BF16 rows x [M,C]."""
+    import torch
+    _need("x", x, (torch.bfloat16,), (-1, -1))
+    M, C = x.shape
+    with _On(x.device):
+        codes = torch.empty((M, C), dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty((M, -(-C // SCALE_BLOCK)), dtype=torch.float8_e8m0fnu,
+                             device=x.device)
+        _check(lib().qgg_fp8_quantize(_ptr(x), M, C, _ptr(codes), _ptr(scales), _stream()),
+               "qgg_fp8_quantize")
+    return codes, scales
+
+
+def fp8_dequantize(codes, scales):
+    """BF16 rows [M,C] from codes [M,C] and scales [M,ceil(C/128)]."""
+    import torch
+    ct, st = _code_types()
+    _need("codes", codes, ct, (-1, -1))
+    M, C = codes.shape
+    _need("scales", scales, st, (M, -(-C // SCALE_BLOCK)), codes.device)
+    with _On(codes.device):
+        x = torch.empty((M, C), dtype=torch.bfloat16, device=codes.device)
+        _check(lib().qgg_fp8_dequantize(_ptr(codes), _ptr(scales), M, C, _ptr(x), _stream()),
+               "qgg_fp8_dequantize")
+    return x
+
+
+@dataclass
+class Fp8Weight:
+    """Frozen 8-bit expert weights on the device: E4M3 codes [E,N,K] (float8_e4m3fn or uint8) and
+    a scale per 128 x 128 block [E,ceil(N/128),K/128] (float8_e8m0fnu or uint8: E8M0; float32)."""
+    codes: "object"
+    scales: "object"
+
+    def __post_init__(self):
+        import torch
+        ct, st = _code_types()
+        _need("codes", self.codes, ct, (-1, -1, -1))
+        E, N, K = self.codes.shape
+        if K % SCALE_BLOCK:
+            raise QggError(f"codes: K = {K}, want a multiple of {SCALE_BLOCK}")
+        _need("scales", self.scales, (*st, torch.float32),
+              (E, -(-N // SCALE_BLOCK), K // SCALE_BLOCK), self.codes.device)
+
+    @property
+    def E(self):
+        return self.codes.shape[0]
+
+    @property
+    def N(self):
+        return self.codes.shape[1]
+
+    @property
+    def K(self):
+        return self.codes.shape[2]
+
+    def c(self):
+        import torch
+        return _Fp8Weight(self.E, self.N, self.K, int(self.scales.dtype == torch.float32),
+                          self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def fp8_grouped_gemm(w: Fp8Weight, a, a_scales, perm: Perm, T: int, k: int, flags: int = A_TOKENS,
+                     out=None):
+    """y [P,N] BF16 in sorted order for 8-bit rows a, a_scales (fp8_quantize) of K columns, or
+    [P,K] for rows of N columns with TRANSPOSE_W; T rows with A_TOKENS, else P = T k."""
+    import torch
+    ct, st = _code_types()
+    trans = bool(flags & TRANSPOSE_W)
+    red, cols = (w.N, w.K) if trans else (w.K, w.N)
+    P = T * k
+    rows = T if flags & A_TOKENS else P
+    dev = w.codes.device
+    _need("a", a, ct, (rows, red), dev)
+    _need("a_scales", a_scales, st, (rows, -(-red // SCALE_BLOCK)), dev)
+    _need_perm(perm, P, dev, w.E)
+    if out is not None:
+        _need("out", out, (torch.bfloat16,), (P, cols), dev)
+    with _On(dev):
+        y = out if out is not None else torch.empty((P, cols), dtype=torch.bfloat16, device=dev)
+        wc, pc = w.c(), perm.c()
+        _check(lib().fp8_grouped_gemm(ctypes.byref(wc), _ptr(a), _ptr(a_scales), flags,
+                                      ctypes.byref(pc), T, k, _ptr(y), _stream()),
+               "fp8_grouped_gemm")
+    return y
+
+
+def swiglu_fp8(h, perm: Perm | None = None, want=("a8", "h8")):
+    """SwiGLU of routed rows h [P,2I] BF16: {"a": BF16 [P,I], "a8"/"a8_scales": the output in 8
+    bits, "h8"/"h8_scales": the rows' 8-bit checkpoint}, those in `want`.  With `perm`, rows
+    past the permutation's last are left as they are."""
+    import torch
+    _need("h", h, (torch.bfloat16,), (-1, -1))
+    P, width = h.shape
+    inter = width // 2
+    if width != 2 * inter or not set(want) <= {"a", "a8", "h8"}:
+        raise QggError(f"h: {width} columns, want an even number; want: {want}")
+    dev = h.device
+    if perm is not None:
+        _need_perm(perm, P, dev)
+    nb = -(-inter // SCALE_BLOCK)
+    r = dict.fromkeys(("a", "a8", "a8_scales", "h8", "h8_scales"))
+    with _On(dev):
+        if "a" in want:
+            r["a"] = torch.empty((P, inter), dtype=torch.bfloat16, device=dev)
+        for name, n in (("a8", 1), ("h8", 2)):
+            if name in want:
+                r[name] = torch.empty((P, n * inter), dtype=torch.float8_e4m3fn, device=dev)
+                r[name + "_scales"] = torch.empty((P, n * nb), dtype=torch.float8_e8m0fnu,
+                                                  device=dev)
+        live = None if perm is None else ctypes.c_void_p(
+            perm.offsets.data_ptr() + 4 * (perm.offsets.numel() - 1))
+        _check(lib().moe_swiglu_fp8(_ptr(h), live, P, inter, _ptr(r["a"]), _ptr(r["a8"]),
+                                    _ptr(r["a8_scales"]), _ptr(r["h8"]), _ptr(r["h8_scales"]),
+                                    _stream()), "moe_swiglu_fp8")
+    return r
+
+
+def swiglu_fp8_bwd(da, h8, h8_scales, topk_gates, perm: Perm, want=("dh8", "dgates")):
+    """From the checkpoint h8 [P,2I] and da [P,I] BF16 (the gradient of the SwiGLU output before
+    the gate): {"dh": BF16 [P,2I], "dh8"/"dh8_scales": the same in 8 bits, "dgates": fp32
+    [T,k]}, those in `want`; topk_gates fp32 [T,k]."""
+    import torch
+    ct, st = _code_types()
+    _need("topk_gates", topk_gates, (torch.float32,), (-1, -1))
+    T, k = topk_gates.shape
+    P = T * k
+    dev = topk_gates.device
+    _need("da", da, (torch.bfloat16,), (P, -1), dev)
+    inter = da.shape[1]
+    nb = -(-inter // SCALE_BLOCK)
+    _need("h8", h8, ct, (P, 2 * inter), dev)
+    _need("h8_scales", h8_scales, st, (P, 2 * nb), dev)
+    _need_perm(perm, P, dev)
+    if not set(want) <= {"dh", "dh8", "dgates"}:
+        raise QggError(f"want: {want}")
+    r = dict.fromkeys(("dh", "dh8", "dh8_scales", "dgates"))
+    with _On(dev):
+        if "dh" in want:
+            r["dh"] = torch.empty((P, 2 * inter), dtype=torch.bfloat16, device=dev)
+        if "dh8" in want:
+            r["dh8"] = torch.empty((P, 2 * inter), dtype=torch.float8_e4m3fn, device=dev)
+            r["dh8_scales"] = torch.empty((P, 2 * nb), dtype=torch.float8_e8m0fnu, device=dev)
+        if "dgates" in want:
+            r["dgates"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+        pc = perm.c()
+        _check(lib().moe_swiglu_fp8_bwd(_ptr(da), _ptr(h8), _ptr(h8_scales), _ptr(topk_gates),
+                                        ctypes.byref(pc), T, k, inter, _ptr(r["dh"]),
+                                        _ptr(r["dh8"]), _ptr(r["dh8_scales"]), _ptr(r["dgates"]),
+                                        _stream()), "moe_swiglu_fp8_bwd")
+    return r
+
+
+def moe_combine(rows, perm: Perm, T: int, k: int, topk_gates=None):
+    """y [T,d] BF16: the sorted rows [P,d] of each token's pairs, weighted by topk_gates [T,k] (or
+    summed)."""
+    import torch
+    _need("rows", rows, (torch.bfloat16,), (T * k, -1))
+    dev = rows.device
+    _need_perm(perm, T * k, dev)
+    if topk_gates is not None:
+        _need("topk_gates", topk_gates, (torch.float32,), (T, k), dev)
+    d = rows.shape[1]
+    with _On(dev):
+        y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+        pc = perm.c()
+        _check(lib().moe_combine(_ptr(rows), d, ctypes.byref(pc), _ptr(topk_gates), T, k, _ptr(y),
+                                 _stream()), "moe_combine")
+    return y

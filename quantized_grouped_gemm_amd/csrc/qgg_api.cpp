@@ -30,6 +30,9 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int kMaxLoraRank = 128;
+constexpr int64_t kMaxRows = (int64_t)1 << 31;   // rows of an 8-bit row tensor
+constexpr int kMaxReduced = 32768;               // reduced width of an 8-bit product
+constexpr int kMaxInter = 1 << 24;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Bump allocator over the caller's workspace.
@@ -862,6 +865,157 @@ qgg_status moe_ffn_bwd_lora(const qgg_qweight* w_gate_up, const qgg_qweight* w_d
   }
   if (dx) QGG_HIP(launch_combine(dxp, d, p->inv_perm, nullptr, T, k, dx, stream,
                                  lgu ? dx_share : nullptr));
+  return QGG_OK;
+}
+
+// ---- scored routing and 8-bit floating point
+
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+static RouteOpts route_opts(const qgg_route_opts* o) {
+  return RouteOpts{o->score == QGG_SCORE_SOFTMAX, o->n_group, o->topk_group, o->group_top,
+                   o->renorm != 0, o->scale};
+}
+
+static bool valid_score(const qgg_route_opts* o, int logits_type) {
+  return o && (o->score == QGG_SCORE_SOFTMAX || o->score == QGG_SCORE_SIGMOID) &&
+         (logits_type == QGG_F32 || logits_type == QGG_BF16) && std::isfinite(o->scale);
+}
+
+qgg_status moe_route_scored(const void* logits, int logits_type, const float* bias, int T, int E,
+                            int k, const qgg_route_opts* opts, int32_t* topk_ids,
+                            float* topk_gates, int32_t* err_flag, qgg_stream_t stream) {
+  if (!valid_route_dims(T, E, k) || !valid_score(opts, logits_type)) return QGG_ERR_INVALID_ARG;
+  const int G = opts->n_group;
+  if (G < 1 || G > E || E % G || opts->topk_group < 1 || opts->topk_group > G ||
+      opts->group_top < 1 || opts->group_top > 2 || opts->group_top > E / G ||
+      (int64_t)opts->topk_group * (E / G) < k)
+    return QGG_ERR_INVALID_ARG;
+  if (opts->topk_group < G && G > 64) return QGG_ERR_UNSUPPORTED;
+  if (T > 0 && (!logits || !topk_ids || !topk_gates)) return QGG_ERR_INVALID_ARG;
+  QGG_HIP(launch_route_scored(logits, logits_type == QGG_BF16, bias, T, E, k, route_opts(opts),
+                              topk_ids, topk_gates, err_flag, stream));
+  return QGG_OK;
+}
+
+qgg_status moe_route_scored_bwd(const void* logits, int logits_type, const int32_t* topk_ids,
+                                const float* dgates, int T, int E, int k,
+                                const qgg_route_opts* opts, void* dlogits, qgg_stream_t stream) {
+  if (!valid_route_dims(T, E, k) || !valid_score(opts, logits_type)) return QGG_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_ids || !dgates || !dlogits)) return QGG_ERR_INVALID_ARG;
+  QGG_HIP(launch_route_scored_bwd(logits, logits_type == QGG_BF16, topk_ids, dgates, T, E, k,
+                                  route_opts(opts), dlogits, stream));
+  return QGG_OK;
+}
+
+qgg_status qgg_fp8_quantize(const uint16_t* x, int64_t rows, int cols, uint8_t* codes,
+                            uint8_t* scales, qgg_stream_t stream) {
+  if (rows < 0 || cols <= 0) return QGG_ERR_INVALID_ARG;
+  if (cols % 8 || rows > kMaxRows) return QGG_ERR_UNSUPPORTED;
+  if (rows > 0 && (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)))
+    return QGG_ERR_INVALID_ARG;
+  QGG_HIP(launch_fp8_quantize(x, rows, cols, codes, scales, stream));
+  return QGG_OK;
+}
+
+qgg_status qgg_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                              uint16_t* x, qgg_stream_t stream) {
+  if (rows < 0 || cols <= 0) return QGG_ERR_INVALID_ARG;
+  if (cols % 8 || rows > kMaxRows) return QGG_ERR_UNSUPPORTED;
+  if (rows > 0 && (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)))
+    return QGG_ERR_INVALID_ARG;
+  QGG_HIP(launch_fp8_dequantize(codes, scales, rows, cols, x, stream));
+  return QGG_OK;
+}
+
+qgg_status fp8_grouped_gemm(const qgg_fp8_weight* w, const uint8_t* a, const uint8_t* a_scales,
+                            int flags, const qgg_perm* p, int T, int k, uint16_t* y,
+                            qgg_stream_t stream) {
+  if (!w || !w->codes || !w->scales || w->N <= 0 || w->K <= 0 ||
+      (w->scale_type != QGG_SCALE_E8M0 && w->scale_type != QGG_SCALE_F32))
+    return QGG_ERR_INVALID_ARG;
+  if (!valid_route_dims(T, w->E, k) || !valid_perm(p, (int64_t)T * k)) return QGG_ERR_INVALID_ARG;
+  if (flags & ~(QGG_A_TOKENS | QGG_TRANSPOSE_W)) return QGG_ERR_INVALID_ARG;
+  if (w->K % 128 || w->N % 64) return QGG_ERR_UNSUPPORTED;
+  if (T > 0 && (!a || !a_scales || !y)) return QGG_ERR_INVALID_ARG;
+  if (!aligned16(w->codes) || !aligned16(a) || !aligned16(y) ||
+      (w->scale_type == QGG_SCALE_F32 && (reinterpret_cast<uintptr_t>(w->scales) & 3)))
+    return QGG_ERR_INVALID_ARG;
+  const int64_t P = (int64_t)T * k;
+  const bool trans = flags & QGG_TRANSPOSE_W, tokens = flags & QGG_A_TOKENS;
+  const int red = trans ? w->N : w->K;
+  const int64_t rows = tokens ? T : P;
+  constexpr int64_t kMost = 0xFFFFFFF0;          // 32-bit buffer offsets, the top 16 kept for "outside"
+  if (red > kMaxReduced || rows * red >= kMost || (int64_t)w->N * w->K >= kMost)
+    return QGG_ERR_UNSUPPORTED;
+  if (P == 0) return QGG_OK;
+  Fp8GemmArgs g;
+  g.w = w->codes;
+  g.w_scales = w->scales;
+  g.w_f32 = w->scale_type == QGG_SCALE_F32;
+  g.E = w->E;
+  g.N = w->N;
+  g.K = w->K;
+  g.trans = trans;
+  g.a = a;
+  g.a_scales = a_scales;
+  g.a_rows = rows;
+  g.tokens = tokens;
+  g.topk = k;
+  g.counts = p->counts;
+  g.offsets = p->offsets;
+  g.perm = p->perm;
+  g.P = P;
+  g.T = T;
+  g.y = y;
+  QGG_HIP(launch_fp8_gemm(g, stream));
+  return QGG_OK;
+}
+
+qgg_status moe_swiglu_fp8(const uint16_t* h, const int32_t* n_rows, int64_t P, int inter,
+                          uint16_t* a, uint8_t* a8, uint8_t* a8_scales, uint8_t* h8,
+                          uint8_t* h8_scales, qgg_stream_t stream) {
+  if (P < 0 || inter <= 0) return QGG_ERR_INVALID_ARG;
+  if (inter % 128 || P > kMaxRows || inter > kMaxInter) return QGG_ERR_UNSUPPORTED;
+  if (P == 0) return QGG_OK;
+  if (!a && !a8 && !h8) return QGG_ERR_INVALID_ARG;
+  if ((a8 && !a8_scales) || (h8 && !h8_scales) || !h) return QGG_ERR_INVALID_ARG;
+  if (!aligned16(h) || !aligned16(a) || !aligned16(a8) || !aligned16(h8))
+    return QGG_ERR_INVALID_ARG;
+  QGG_HIP(launch_swiglu_fp8(h, n_rows, P, inter, a, a8, a8_scales, h8, h8_scales, stream));
+  return QGG_OK;
+}
+
+qgg_status moe_swiglu_fp8_bwd(const uint16_t* da, const uint8_t* h8, const uint8_t* h8_scales,
+                              const float* topk_gates, const qgg_perm* p, int T, int k, int inter,
+                              uint16_t* dh, uint8_t* dh8, uint8_t* dh8_scales, float* dgates,
+                              qgg_stream_t stream) {
+  if (T < 0 || k < 1 || k > 32 || (int64_t)T * k >= (int64_t)1 << 31 || inter <= 0)
+    return QGG_ERR_INVALID_ARG;
+  const int64_t P = (int64_t)T * k;
+  if (!valid_perm(p, P)) return QGG_ERR_INVALID_ARG;
+  if (inter % 128 || inter > kMaxInter) return QGG_ERR_UNSUPPORTED;
+  if (P == 0) return QGG_OK;
+  if (!dh && !dh8 && !dgates) return QGG_ERR_INVALID_ARG;
+  if (dh8 && !dh8_scales) return QGG_ERR_INVALID_ARG;
+  if (!da || !h8 || !h8_scales || !topk_gates) return QGG_ERR_INVALID_ARG;
+  if (!aligned16(da) || !aligned16(h8) || !aligned16(dh) || !aligned16(dh8))
+    return QGG_ERR_INVALID_ARG;
+  QGG_HIP(launch_swiglu_fp8_bwd(da, h8, h8_scales, topk_gates, p->inv_perm, P, inter, dh, dh8,
+                                dh8_scales, dgates, stream));
+  return QGG_OK;
+}
+
+qgg_status moe_combine(const uint16_t* rows, int d, const qgg_perm* p, const float* topk_gates,
+                       int T, int k, uint16_t* y, qgg_stream_t stream) {
+  if (T < 0 || k < 1 || k > 32 || (int64_t)T * k >= (int64_t)1 << 31 || d <= 0 ||
+      !valid_perm(p, (int64_t)T * k))
+    return QGG_ERR_INVALID_ARG;
+  if (d % 8) return QGG_ERR_UNSUPPORTED;
+  if (T > 0 && (!rows || !y)) return QGG_ERR_INVALID_ARG;
+  if (!aligned16(rows) || !aligned16(y)) return QGG_ERR_INVALID_ARG;
+  if (T == 0) return QGG_OK;
+  QGG_HIP(launch_combine(rows, d, p->inv_perm, topk_gates, T, k, y, stream));
   return QGG_OK;
 }
 

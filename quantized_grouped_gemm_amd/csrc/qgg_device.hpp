@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace qgg {
 
 constexpr int kWave = 64;
@@ -66,6 +68,36 @@ __device__ __forceinline__ int block_excl_scan(int v, int* lds, int* total) {
   return before + incl - v;
 }
 
+// Wavefront maximum of a 64-bit key through DPP row/quad moves (no LDS round
+// trips); the result is read from lane 63.
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t k) {
+  auto step = [&](auto ctrl_c, auto rmask_c) {
+    constexpr int kCtrl = decltype(ctrl_c)::value;
+    constexpr int kRow = decltype(rmask_c)::value;
+    const uint32_t lo = (uint32_t)k, hi = (uint32_t)(k >> 32);
+    const uint32_t olo = __builtin_amdgcn_update_dpp(lo, lo, kCtrl, kRow, 0xF, false);
+    const uint32_t ohi = __builtin_amdgcn_update_dpp(hi, hi, kCtrl, kRow, 0xF, false);
+    const uint64_t o = ((uint64_t)ohi << 32) | olo;
+    k = o > k ? o : k;
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});   // quad_perm 1,0,3,2
+  step(integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});   // quad_perm 2,3,0,1
+  step(integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});  // row_half_mirror
+  step(integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});  // row_mirror
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast:15
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast:31
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)k, 63);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(k >> 32), 63);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// fp32 -> uint32 with the same order (larger float, larger key)
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
 // E8M0 exponent code -> fp32 scale 2^(c-127); code 0 is the subnormal 2^-127,
 // code 255 is NaN.
 __device__ __forceinline__ float e8m0_to_f32(uint32_t c) {
@@ -122,6 +154,14 @@ __device__ __forceinline__ uint2 lds_tr4(const uint8_t* p) {
 // outstanding and all LDS operations are done (gfx9 encoding: vmcnt in bits
 // [3:0] and [15:14], expcnt [6:4] left at its maximum, lgkmcnt [11:8] = 0).
 constexpr int vm_lgkm0_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4); }
+
+// Orders LDS accesses among the lanes of one wavefront (its LDS operations
+// execute in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Compiler-only fence: no memory access moves across it; emits nothing.
 __device__ __forceinline__ void compiler_fence() { asm volatile("" ::: "memory"); }

@@ -149,6 +149,54 @@ hipError_t launch_lora_bwd_gated(const uint16_t* a, int K, int N, int E, const i
                                  float* us, uint16_t* dx, float* dA, float* dB, int64_t P,
                                  hipStream_t s);
 
+// Scored routing (route_scored.hip).
+struct RouteOpts {
+  bool softmax;                  // else sigmoid
+  int n_group, topk_group, group_top;
+  bool renorm;
+  float scale;
+};
+hipError_t launch_route_scored(const void* logits, bool bf16, const float* bias, int T, int E,
+                               int k, const RouteOpts& o, int32_t* ids, float* gates, int32_t* err,
+                               hipStream_t s);
+hipError_t launch_route_scored_bwd(const void* logits, bool bf16, const int32_t* ids,
+                                   const float* dgates, int T, int E, int k, const RouteOpts& o,
+                                   void* dlogits, hipStream_t s);
+
+// FP8 rows (fp8_rows.hip): E4M3 codes with one E8M0 scale per 128 columns;
+// rows at and past *n_rows (nullable) are left as they are.
+hipError_t launch_fp8_quantize(const uint16_t* x, int64_t rows, int cols, uint8_t* codes,
+                               uint8_t* scales, hipStream_t s);
+hipError_t launch_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                 int cols, uint16_t* x, hipStream_t s);
+hipError_t launch_swiglu_fp8(const uint16_t* h, const int32_t* n_rows, int64_t P, int inter,
+                             uint16_t* a, uint8_t* a8, uint8_t* a_scales, uint8_t* h8,
+                             uint8_t* h_scales, hipStream_t s);
+hipError_t launch_swiglu_fp8_bwd(const uint16_t* da, const uint8_t* h8, const uint8_t* h_scales,
+                                 const float* gates, const int32_t* inv_perm, int64_t P, int inter,
+                                 uint16_t* dh, uint8_t* dh8, uint8_t* dh_scales, float* dgates,
+                                 hipStream_t s);
+
+// FP8 grouped product (fp8_gemm.hip).
+struct Fp8GemmArgs {
+  const uint8_t* w;              // [E][N][K]
+  const void* w_scales;          // [E][ceil(N/128)][K/128]
+  bool w_f32;                    // fp32 scales, else E8M0
+  int E, N, K;
+  bool trans;                    // y = a W (reduce over N), else y = a W^T
+  const uint8_t* a;              // rows of the reduced width
+  const uint8_t* a_scales;       // [rows][ceil(width/128)]
+  int64_t a_rows;
+  bool tokens;                   // sorted row i reads a row perm[i] / topk, else row i
+  int topk;
+  const int32_t* counts;
+  const int32_t* offsets;
+  const int32_t* perm;
+  int64_t P, T;
+  uint16_t* y;                   // [P][N] or [P][K]
+};
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t s);
+
 int num_cus();
 
 // Measurement hook (qgg_set_timing_events): while the calling thread has

@@ -10,41 +10,9 @@
 #include "qgg_device.hpp"
 #include "qgg_internal.hpp"
 
-#include <type_traits>
-
 namespace qgg {
 
 // ---------------------------------------------------------------- route
-// Wavefront maximum of a 64-bit key through DPP row/quad moves (no LDS round
-// trips); the result is read from lane 63.
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t k) {
-  auto step = [&](auto ctrl_c, auto rmask_c) {
-    constexpr int kCtrl = decltype(ctrl_c)::value;
-    constexpr int kRow = decltype(rmask_c)::value;
-    const uint32_t lo = (uint32_t)k, hi = (uint32_t)(k >> 32);
-    const uint32_t olo = __builtin_amdgcn_update_dpp(lo, lo, kCtrl, kRow, 0xF, false);
-    const uint32_t ohi = __builtin_amdgcn_update_dpp(hi, hi, kCtrl, kRow, 0xF, false);
-    const uint64_t o = ((uint64_t)ohi << 32) | olo;
-    k = o > k ? o : k;
-  };
-  using std::integral_constant;
-  step(integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});   // quad_perm 1,0,3,2
-  step(integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});   // quad_perm 2,3,0,1
-  step(integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});  // row_half_mirror
-  step(integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});  // row_mirror
-  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast:15
-  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast:31
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)k, 63);
-  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(k >> 32), 63);
-  return ((uint64_t)hi << 32) | lo;
-}
-
-// fp32 -> uint32 with the same order (larger float, larger key)
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t u = __float_as_uint(v);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
 // One wavefront per token.  Each lane holds NV logits (experts lane, lane +
 // 64, ...; NV * 64 >= E); k rounds of a wavefront arg-max under the key
 // (logit desc, id asc) pick the experts, each lane offering its best
