@@ -451,8 +451,8 @@ typedef struct {
  * QGG_A_TOKENS, else P; products and sums in fp32, y BF16 in sorted order.
  * Rows of y at and past offsets[E] are left as they are.  The call needs no
  * workspace, so calls on different streams need nothing of their own.
- * K % 128 == 0, N % 64 == 0, the reduced width at most 32768, N * K and a's
- * bytes below 2^32 - 16, else QGG_ERR_UNSUPPORTED; codes, a and y 16-byte
+ * K % 128 == 0, N % 64 == 0, the reduced width at most 32768, (N + 64) * K and
+ * a's bytes below 2^32 - 2^16, else QGG_ERR_UNSUPPORTED; codes, a and y 16-byte
  * aligned.  Deterministic. */
 qgg_status fp8_grouped_gemm(const qgg_fp8_weight* w, const uint8_t* a, const uint8_t* a_scales,
                             int flags, const qgg_perm* p, int T, int k, uint16_t* y,

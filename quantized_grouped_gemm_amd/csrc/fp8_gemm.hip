@@ -12,8 +12,8 @@
 // Operands: W is the MFMA's A matrix (16 output columns), the activation rows
 // its B matrix (16 rows), so a lane ends with four consecutive output columns
 // of one row.  The order of the 128 reduced values inside an MFMA is free as
-// long as both operands share it: lane (i, q) holds bytes 16 q .. 16 q + 15 of
-// the first and of the second 64.
+// long as both operands share it: lane (i, q) holds the 32 bytes from 64 (q &
+// 1) + 32 (q / 2) of its row.
 #include "qgg_device.hpp"
 #include "qgg_internal.hpp"
 
@@ -26,8 +26,16 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
 
 
-// Tile row r of an LDS stage is 128 bytes; its 16-byte chunk c sits at slot c ^
-// (r & 7), so that eight consecutive rows' reads of one chunk hit distinct banks.
+// LDS has 64 banks of four bytes, so 16 lanes reading 16 bytes each are served
+// at once if they touch each 16-byte slot of 256 bytes once.  Chunk c of a row
+// sits at slot c ^ swz(row); the swizzles make the 16 lanes of an operand read
+// (and the 32 of a transposing one) touch them all:
+// activation rows r = 16 mb + 0 .. 15, 128 bytes each
+__device__ __forceinline__ int swz_a(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
+// columns 64 g + 16 (i / 4) + 4 nb + i % 4 of W, i = 0 .. 15, 128 bytes each
+__device__ __forceinline__ int swz_w(int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); }
+// rows of W r0 + 0 .. 7 and r0 + 64 .. 71, 64 bytes each
+__device__ __forceinline__ int swz_t(int r) { return ((r >> 1) & 2) | ((r >> 6) & 1); }
 
 // Eight rows x 16 columns of bytes by a transposing LDS read: within each
 // 16-lane group, lane p points at eight bytes (row p / 2, half p & 1) and
@@ -37,7 +45,7 @@ __device__ __forceinline__ i32x2_t lds_tr8(const uint8_t* p) {
 }
 
 // first[e] = tiles of up to MT rows of the experts before e, first[E] = all of
-// them (256 threads, four experts each; E <= 1024).
+// them (four experts a thread; E <= 1024, at least 256 threads).
 __device__ __forceinline__ void count_tiles(const int32_t* counts, int E, int MT, int* first,
                                             int* scratch) {
   int n[4], sum = 0;
@@ -56,16 +64,23 @@ __device__ __forceinline__ void count_tiles(const int32_t* counts, int E, int MT
   __syncthreads();
 }
 
-// Tile number t: the thread that looks at its expert leaves {expert, row0,
-// rows} in out.
-__device__ __forceinline__ void find_tile(int t, const int* first, const int32_t* counts,
-                                          const int32_t* offsets, int E, int MT, int* out) {
-  for (int e = threadIdx.x; e < E; e += 256) {
-    const int k = t - first[e];
-    if (k >= 0 && t < first[e + 1]) {
+// Item i: experts ascending, in an expert column group by column group, and
+// the tiles of a column group side by side, so that the workgroups which read
+// the same weights do so at the same time and share them in their L2.  The
+// thread that looks at its expert leaves {expert, row0, rows, column group}.
+__device__ __forceinline__ void find_item(int i, int ntn, const int* first, const int32_t* counts,
+                                          const int32_t* offsets, int E, int* out) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    const int f = first[e], n = first[e + 1] - f;
+    const int p = i - f * ntn;
+    if (p >= 0 && p < n * ntn) {
+      const int nt = p / n, k = p - nt * n;
+      const int c = counts[e], blocks = (c + 15) >> 4;     // split into equal numbers of blocks
+      const int b0 = k * blocks / n, b1 = (k + 1) * blocks / n;
       out[0] = e;
-      out[1] = offsets[e] + k * MT;
-      out[2] = min(MT, counts[e] - k * MT);
+      out[1] = offsets[e] + 16 * b0;
+      out[2] = min(16 * b1, c) - 16 * b0;
+      out[3] = nt;
     }
   }
 }
@@ -73,14 +88,64 @@ __device__ __forceinline__ void find_tile(int t, const int* first, const int32_t
 // Stages in the LDS ring of activation tiles, and weight steps in flight per
 // wavefront in registers (one step is 64 columns x 128 = 8 KiB).
 constexpr int kNBuf = 4;
-template <int MB>
-constexpr int w_ring() { return 2; }
+constexpr int kRing = 2;
 
-// One reduction step of a wavefront's 16 NB columns of W.
-template <int NB>
+// One reduction step of a wavefront's 64 columns of W, as MFMA operands.
 struct WStep {
-  i32x8_t w[NB];
+  i32x8_t w[4];
 };
+
+// The same as it is loaded.  Memory is read fastest where the four lanes of a
+// quad take 64 consecutive bytes, while an MFMA operand wants a lane to hold
+// one row: with one row a lane, every 16-byte piece is a cache access of its
+// own, and those bound the kernel (64 accesses a load, 84 % of all cycles).  So
+// lane 16 q + 4 a + p of load j of a pair of 16-row blocks (X, Y) takes chunk
+// p of half q & 1 of row 4 a + j of block q < 2 ? X : Y; a 4 x 4 transposition
+// in each quad gives the lane row 4 a + p's four chunks, and an exchange of
+// the wavefront's halves splits them between X's operand and Y's.
+struct WRaw {
+  u32x4_t r[2][4];                               // [pair][j]
+};
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+// Operands of one pair of blocks (x: the first, y: the second).
+struct WPair {
+  i32x8_t x, y;
+};
+
+__device__ __forceinline__ WPair to_operands(const u32x4_t (&raw)[4], int lane) {
+  const bool odd1 = lane & 1, odd2 = lane & 2;
+  WPair out;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {                // exchange bit 1 of j and of the lane
+      const uint32_t x = raw[j][d], y = raw[j + 2][d];
+      const uint32_t mx = quad_move<0x4E>(x), my = quad_move<0x4E>(y);
+      v[j] = odd2 ? my : x;
+      v[j + 2] = odd2 ? y : mx;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {             // bit 0
+      const uint32_t x = v[j], y = v[j + 1];
+      const uint32_t mx = quad_move<0xB1>(x), my = quad_move<0xB1>(y);
+      v[j] = odd1 ? my : x;
+      v[j + 1] = odd1 ? y : mx;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const auto sw = __builtin_amdgcn_permlane32_swap(v[t], v[t + 2], false, false);
+      out.x[4 * t + d] = (int)sw[0];
+      out.y[4 * t + d] = (int)sw[1];
+    }
+  }
+  return out;
+}
 
 struct Item {
   int expert, row0, nrows, nt;
@@ -98,7 +163,7 @@ struct RowCopy {
   __device__ __forceinline__ void init(const Fp8GemmArgs& g, const Item& it, int red) {
     a = g.a;
     bytes = (uint32_t)(g.a_rows * red);
-    col = ((threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7)) * 16;
+    col = ((threadIdx.x & 7) ^ swz_a(threadIdx.x >> 3)) * 16;
 #pragma unroll
     for (int i = 0; i < NCA; ++i) {
       const int r = 32 * i + (threadIdx.x >> 3);
@@ -167,30 +232,27 @@ __device__ __forceinline__ void stage_w_scales(const void* scales, int64_t at, i
   }
 }
 
-// MB scale bytes of a lane as MFMA scale operands: block mb is byte mb & 3 of
-// word mb / 4.
+// MB scale bytes of a lane as MFMA scale operand: block mb is byte mb.
 template <int MB>
 __device__ __forceinline__ void read_scales(const uint8_t* sc, int st, int i16, int x[2]) {
   const uint8_t* at = sc + (st * 16 + i16) * MB;
-  if constexpr (MB == 8) {
-    const uint2 v = *reinterpret_cast<const uint2*>(at);
-    x[0] = (int)v.x;
-    x[1] = (int)v.y;
-  } else if constexpr (MB == 4) {
+  if constexpr (MB == 4) {
     x[0] = *reinterpret_cast<const int*>(at);
   } else {
     x[0] = *reinterpret_cast<const uint16_t*>(at);
   }
 }
 
-// Rows of block mb; `at` = lane's offset of chunk q in row i16
+// Rows of block mb; `at` = offset of the first of the lane's two chunks
 __device__ __forceinline__ i32x8_t read_rows(const uint8_t* as, int mb, int at) {
   const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(as + mb * 2048 + at);
-  const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(as + mb * 2048 + (at ^ 64));
+  const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(as + mb * 2048 + (at ^ 16));
   return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                  (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
-__device__ __forceinline__ int rows_at(int i16, int q) { return i16 * 128 + ((q ^ (i16 & 7)) << 4); }
+__device__ __forceinline__ int rows_at(int i16, int q) {
+  return i16 * 128 + (((4 * (q & 1) + 2 * (q >> 1)) ^ swz_a(i16)) << 4);
+}
 
 // acc += scales * (W block . rows of block mb)
 template <bool WF32, int SEL>
@@ -210,9 +272,9 @@ __device__ __forceinline__ void mfma_block(const i32x8_t& w, const i32x8_t& x, u
 // One reduction step: the operand rows of the next 16-row block are read from
 // LDS while the matrix core works on this one's (the group barriers pin two
 // reads, four MFMAs, two reads, ...).
-template <bool WF32, int NMB, int NB>
-__device__ __forceinline__ void mfma_step(const uint8_t* as, const WStep<NB>& w, uint32_t ws, const int xs[2],
-                                          int at, f32x4_t (&acc)[NMB][NB]) {
+template <bool WF32, int NMB>
+__device__ __forceinline__ void mfma_step(const uint8_t* as, const WStep& w, uint32_t ws,
+                                          const int xs[2], int at, f32x4_t (&acc)[NMB][4]) {
   using std::integral_constant;
   i32x8_t x = read_rows(as, 0, at);
   auto row_block = [&](auto mbc) {
@@ -221,7 +283,7 @@ __device__ __forceinline__ void mfma_step(const uint8_t* as, const WStep<NB>& w,
       i32x8_t nx = x;
       if constexpr (mb + 1 < NMB) nx = read_rows(as, mb + 1, at);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < 4; ++nb)
         mfma_block<WF32, (mb & 3)>(w.w[nb], x, ws, xs[mb >> 2], acc[mb][nb]);
       x = nx;
     }
@@ -236,14 +298,14 @@ __device__ __forceinline__ void mfma_step(const uint8_t* as, const WStep<NB>& w,
   row_block(integral_constant<int, 7>{});
 }
 
-template <bool WF32, int NMB, int NB>
+template <bool WF32, int NMB>
 __device__ __forceinline__ void mfma_schedule() {
   __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
   for (int mb = 0; mb < NMB; ++mb) {
     if (mb + 1 < NMB) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int nb = 0; nb < 4; ++nb) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       if (WF32) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
       if (mb + 1 == NMB) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
@@ -251,18 +313,17 @@ __device__ __forceinline__ void mfma_schedule() {
   }
 }
 
-// One item of y = a W^T: rows [row0, row0 + nrows) of an expert x 64 NB
-// columns, NMB live 16-row blocks.  Weights go from memory straight into the MFMA's A
-// registers, w_ring steps ahead; the rows go through a ring of LDS stages,
+// One item of y = a W^T: rows [row0, row0 + nrows) of an expert x 256
+// columns, NMB live 16-row blocks.  Weights go from memory straight into
+// registers, kRing steps ahead; the rows go through a ring of LDS stages,
 // kNBuf - 1 ahead; the barrier that ends a step waits for the next step's
 // copies only.  The loop is branch-free, four steps a round: past the last step
 // the weights repeat it and the rows are zeros with scale 1, which adds nothing.
-template <bool WF32, int MB, int NMB, int NB>
+template <bool WF32, int MB, int NMB>
 __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, const LdsRing4& As,
                                         uint8_t* sc, uint32_t* wt) {
-  constexpr int kRing = w_ring<MB>();
   constexpr int kNCA = NMB / 2 > 0 ? NMB / 2 : 1;
-  constexpr int kStageLoads = kNCA + 2 * NB;
+  constexpr int kStageLoads = kNCA + 8;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int i16 = lane & 15, q = lane >> 4;
@@ -271,42 +332,35 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
   RowCopy<kNCA> rc;
   rc.init(g, it, g.K);
 
-  // this wavefront's columns, in NB / 4 groups of 64 that share a scale; a
-  // group past the edge repeats the last columns and stores nothing
-  constexpr int kG = NB / 4;
-  const int base = it.nt * 64 * NB + wave * 16 * NB;
-  int cg[kG];
-#pragma unroll
-  for (int j = 0; j < kG; ++j) cg[j] = min(base + 64 * j, g.N - 64);
+  const int base = it.nt * 256 + wave * 64;
+  const bool active = base < g.N;
+  const int cbase = active ? base : g.N - 64;    // a wave past the edge repeats the last columns
   const uint32_t wbytes = (uint32_t)g.N * (uint32_t)g.K;
   const __amdgpu_buffer_rsrc_t wrsrc = raw_buffer(g.w + (int64_t)it.expert * wbytes, wbytes);
-  const int64_t sat = ((int64_t)it.expert * ((g.N + 127) >> 7) + (cg[0] >> 7)) * steps;
-  uint32_t wv[kG];
-#pragma unroll
-  for (int j = 0; j < kG; ++j)
-    wv[j] = (uint32_t)(cg[j] + 16 * (i16 >> 2) + (i16 & 3)) * (uint32_t)g.K + 16 * q;
-  auto load_w = [&](int st, WStep<NB>& w) {
+  const int64_t sat = ((int64_t)it.expert * ((g.N + 127) >> 7) + (cbase >> 7)) * steps;
+  const int a4 = (lane >> 2) & 3, p4 = lane & 3;
+  const uint32_t wv =
+      (uint32_t)(cbase + 16 * a4 + 4 * (q >> 1)) * (uint32_t)g.K + 64 * (q & 1) + 16 * p4;
+  auto load_w = [&](int st, WRaw& w) {
     const int s = st < steps ? st : steps - 1;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const uint32_t so = (uint32_t)s * 128u + (uint32_t)(nb & 3) * 4u * (uint32_t)g.K;
-      const u32x4_t lo = __builtin_amdgcn_raw_buffer_load_b128(wrsrc, wv[nb >> 2], so, 0);
-      const u32x4_t hi = __builtin_amdgcn_raw_buffer_load_b128(wrsrc, wv[nb >> 2], so + 64, 0);
-      w.w[nb] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                        (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-    }
+    for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)                // row 16 a + 4 nb + j
+        w.r[pr][j] = __builtin_amdgcn_raw_buffer_load_b128(
+            wrsrc, wv, (uint32_t)s * 128u + (uint32_t)(8 * pr + j) * (uint32_t)g.K, 0);
   };
 
-  f32x4_t acc[NMB][NB];
+  f32x4_t acc[NMB][4];
 #pragma unroll
   for (int mb = 0; mb < NMB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   using std::integral_constant;
   for (int st0 = 0; st0 < steps; st0 += kPiece) {
     const int n = (min(kPiece, steps - st0) + 3) & ~3;
-    WStep<NB> ring[kRing];
+    WRaw ring[kRing];
     rc.copy_whole(st0, steps, wave, As.b[0]);
     rc.copy_whole(st0 + 1, steps, wave, As.b[1]);
     rc.copy_whole(st0 + 2, steps, wave, As.b[0] + 16 * MB * 128);
@@ -318,13 +372,21 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
     stage_barrier<0>();
     // step i reads stage (i / 2) & 1 of object i & 1 while step i + 3 goes to
     // the other object
-    auto kstage = [&](int i, WStep<NB>& w, const uint8_t* rows, uint8_t* next) {
+    auto kstage = [&](int i, WRaw& raw, const uint8_t* rows, uint8_t* next) {
       rc.copy_whole(st0 + i + kNBuf - 1, steps, wave, next);
       int xs[2];
       read_scales<MB>(sc, i, i16, xs);
-      mfma_step<WF32, NMB, NB>(rows, w, wt[wave * kPiece + i], xs, at, acc);
-      load_w(st0 + i + kRing, w);
-      mfma_schedule<WF32, NMB, NB>();
+      const uint32_t ws = wt[wave * kPiece + i];
+      WStep w;
+#pragma unroll
+      for (int pr = 0; pr < 2; ++pr) {
+        const WPair p = to_operands(raw.r[pr], lane);
+        w.w[2 * pr] = p.x;
+        w.w[2 * pr + 1] = p.y;
+      }
+      mfma_step<WF32, NMB>(rows, w, ws, xs, at, acc);
+      load_w(st0 + i + kRing, raw);
+      mfma_schedule<WF32, NMB>();
       // the copies of step i + 1 were issued two steps ago
       stage_barrier<2 * kStageLoads>();
     };
@@ -340,23 +402,20 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
     __builtin_amdgcn_s_waitcnt(vm_lgkm0_imm(0));
     __syncthreads();
   }
+  if (!active) return;
 #pragma unroll
   for (int mb = 0; mb < NMB; ++mb) {
     const int r = 16 * mb + i16;
     if (r >= it.nrows) continue;
-    // block 4 j + nb holds columns 16 q + 4 nb .. + 3 of group j
+    // block nb holds columns 16 q + 4 nb .. + 3
+    uint16_t* out = g.y + (int64_t)(it.row0 + r) * g.N + cbase + 16 * q;
 #pragma unroll
-    for (int j = 0; j < kG; ++j) {
-      if (base + 64 * j >= g.N) continue;
-      uint16_t* out = g.y + (int64_t)(it.row0 + r) * g.N + cg[j] + 16 * q;
-      const f32x4_t* v = acc[mb] + 4 * j;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4_t*>(out + 8 * h) = u32x4_t{
-            pack_bf16x2(v[2 * h][0], v[2 * h][1]), pack_bf16x2(v[2 * h][2], v[2 * h][3]),
-            pack_bf16x2(v[2 * h + 1][0], v[2 * h + 1][1]),
-            pack_bf16x2(v[2 * h + 1][2], v[2 * h + 1][3])};
-    }
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<u32x4_t*>(out + 8 * h) =
+          u32x4_t{pack_bf16x2(acc[mb][2 * h][0], acc[mb][2 * h][1]),
+                  pack_bf16x2(acc[mb][2 * h][2], acc[mb][2 * h][3]),
+                  pack_bf16x2(acc[mb][2 * h + 1][0], acc[mb][2 * h + 1][1]),
+                  pack_bf16x2(acc[mb][2 * h + 1][2], acc[mb][2 * h + 1][3])};
   }
 }
 
@@ -396,32 +455,32 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
       stage_w_scales<WF32>(g.w_scales, sat, KB, st, n, steps, wt);
     }
     rc.copy_part(st, g.N, wave, as);
-    // slot 4 r + s of a wavefront's 8 KiB holds chunk s ^ (r / 2 & 3) of row r
+    // slot 4 r + s of a wavefront's 8 KiB holds chunk s ^ swz_t(r) of row r
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int slot = 64 * j + lane, r = slot >> 2;
-      const int chunk = (slot & 3) ^ ((r >> 1) & 3);
+      const int chunk = (slot & 3) ^ swz_t(r);
       const uint32_t n = st * 128 + r;
       const uint32_t off = n < (uint32_t)g.N ? n * (uint32_t)g.K + cbase + 16 * chunk : 0xFFFFFFF0u;
       copy16_to_lds(wrsrc, off, 0, mine + j * 1024);
     }
-    WStep<4> w;
+    WStep w;
     __builtin_amdgcn_s_waitcnt(vm_lgkm0_imm(0));
     __syncthreads();
 #pragma unroll
     for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        // reduced values 16 q + 64 (t / 2) + 8 (t & 1) .. + 7, columns 16 nb ..
-        const int r = 16 * q + 64 * (t >> 1) + 8 * (t & 1) + (i16 >> 1);
-        const int slot = r * 4 + (nb ^ ((r >> 1) & 3));
+        // reduced values 64 (q & 1) + 32 (q / 2) + 8 t .. + 7, columns 16 nb ..
+        const int r = 64 * (q & 1) + 32 * (q >> 1) + 8 * t + (i16 >> 1);
+        const int slot = r * 4 + (nb ^ swz_t(r));
         const i32x2_t v = lds_tr8(mine + slot * 16 + (i16 & 1) * 8);
         w.w[nb][2 * t] = v[0];
         w.w[nb][2 * t + 1] = v[1];
       }
     int xs[2];
     read_scales<MB>(sc, st % kPiece, i16, xs);
-    mfma_step<WF32, NMB, 4>(as, w, wt[wave * kPiece + st % kPiece], xs, at, acc);
+    mfma_step<WF32, NMB>(as, w, wt[wave * kPiece + st % kPiece], xs, at, acc);
     __syncthreads();
   }
   if (!active) return;
@@ -439,18 +498,18 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
   }
 }
 
-// Workgroups take items (tile, 64 NB columns) in order, eight interleaved
+// Workgroups take items (tile, 256 columns) in order, eight interleaved
 // stretches of them, one per XCD (workgroup b runs on XCD b mod 8): the columns
 // of a tile and the tiles of an expert then share one L2.
-template <bool TRANS, bool WF32, int MB, int NB>
-__global__ __launch_bounds__(256, NB == 8 ? 1 : 2) void k_fp8_gemm(Fp8GemmArgs g, int ntn) {
+template <bool TRANS, bool WF32, int MB>
+__global__ __launch_bounds__(256, 2) void k_fp8_gemm(Fp8GemmArgs g, int ntn) {
   // separate objects: the compiler tells a copy into one from a read of another
   __shared__ __attribute__((aligned(16))) uint8_t b0[16 * MB * 256];
   __shared__ __attribute__((aligned(16))) uint8_t b1[TRANS ? 32768 : 16 * MB * 256];
   __shared__ __attribute__((aligned(16))) uint8_t sc[kPiece * 16 * MB];
   const LdsRing4 As{{b0, b1, nullptr, nullptr}};
   __shared__ int scratch[16];
-  __shared__ int tile[3];
+  __shared__ int item[4];
   __shared__ uint32_t wt[4 * kPiece];
   __shared__ int tiles_before[1025];
   count_tiles(g.counts, g.E, 16 * MB, tiles_before, scratch);
@@ -458,28 +517,22 @@ __global__ __launch_bounds__(256, NB == 8 ? 1 : 2) void k_fp8_gemm(Fp8GemmArgs g
   const int per = (items + 7) >> 3;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, items);
   for (int i = first + (blockIdx.x >> 3); i < last; i += gridDim.x >> 3) {
-    const int t = i / ntn;
     __syncthreads();
-    find_tile(t, tiles_before, g.counts, g.offsets, g.E, 16 * MB, tile);
+    find_item(i, ntn, tiles_before, g.counts, g.offsets, g.E, item);
     __syncthreads();
     Item it;
-    it.expert = __builtin_amdgcn_readfirstlane(tile[0]);
-    it.row0 = __builtin_amdgcn_readfirstlane(tile[1]);
-    it.nrows = __builtin_amdgcn_readfirstlane(tile[2]);
-    it.nt = i - t * ntn;
+    it.expert = __builtin_amdgcn_readfirstlane(item[0]);
+    it.row0 = __builtin_amdgcn_readfirstlane(item[1]);
+    it.nrows = __builtin_amdgcn_readfirstlane(item[2]);
+    it.nt = __builtin_amdgcn_readfirstlane(item[3]);
     const int live = (it.nrows + 15) >> 4;
     auto run = [&](auto n) {
       constexpr int NMB = decltype(n)::value;
       if constexpr (TRANS) t_item<WF32, MB, NMB>(g, it, b0, b1, sc, wt);
-      else nt_item<WF32, MB, NMB, NB>(g, it, As, sc, wt);
+      else nt_item<WF32, MB, NMB>(g, it, As, sc, wt);
     };
     using std::integral_constant;
-    if constexpr (MB == 8) {
-      if (live > 6) run(integral_constant<int, 8>{});
-      else if (live > 4) run(integral_constant<int, 6>{});
-      else if (live > 2) run(integral_constant<int, 4>{});
-      else run(integral_constant<int, 2>{});
-    } else if constexpr (MB == 4) {
+    if constexpr (MB == 4) {
       if (live > 2) run(integral_constant<int, 4>{});
       else if (live > 1) run(integral_constant<int, 2>{});
       else run(integral_constant<int, 1>{});
@@ -487,6 +540,235 @@ __global__ __launch_bounds__(256, NB == 8 ? 1 : 2) void k_fp8_gemm(Fp8GemmArgs g
       if (live > 1) run(integral_constant<int, 2>{});
       else run(integral_constant<int, 1>{});
     }
+  }
+}
+
+// ---- large tiles
+// 256 rows x 256 columns on eight wavefronts, two (halves of the rows) by four
+// (64 columns each).  Rows and weights both pass through LDS, two stages of 64
+// KiB: every byte that a workgroup asks its L2 for is used by 256 rows or
+// columns, which is what bounds a product of this size (see launch_sized).
+struct BigStage {
+  uint8_t* a;                                    // [256][128]
+  uint8_t* w;                                    // y = a W^T: [256 columns][128]
+};                                               // y = a W: [4 column groups][128][64]
+
+template <bool TRANS, bool WF32, int NMB>
+__device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, const BigStage& s0,
+                                         const BigStage& s1, uint8_t* sc, uint32_t* wt) {
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63;
+  const int i16 = lane & 15, q = lane >> 4;
+  const int half = wave >> 2, nq = wave & 3;
+  const int blocks = (it.nrows + 15) >> 4, h0 = (blocks + 1) >> 1;   // blocks of the first half
+  const int red = TRANS ? g.N : g.K, cols = TRANS ? g.K : g.N;
+  const int steps = (red + 127) >> 7;
+
+  // row copies: slot tid & 7 of rows 64 i + tid / 8
+  const uint32_t abytes = (uint32_t)(g.a_rows * red);
+  const int acol = ((tid & 7) ^ swz_a(tid >> 3)) * 16;
+  uint32_t aoff[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 64 * i + (tid >> 3);
+    const int rr = it.row0 + (r < it.nrows ? r : 0);
+    const uint32_t src = g.tokens ? g.perm[rr] / g.topk : rr;
+    aoff[i] = src * (uint32_t)red + (uint32_t)acol;
+  }
+  // weight copies
+  const uint32_t wbytes = (uint32_t)g.N * (uint32_t)g.K;
+  const uint8_t* wbase = g.w + (int64_t)it.expert * wbytes;
+  uint32_t woff[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (TRANS) {
+      // wavefront: 32 rows of one column group; slot 4 r + s holds chunk s ^ swz_t(r)
+      const int grp = wave >> 1;
+      const int r = (wave & 1) * 64 + 16 * i + (lane >> 2);
+      const int chunk = (lane & 3) ^ swz_t(r);
+      const int c = min(it.nt * 256 + 64 * grp, cols - 64);
+      woff[i] = (uint32_t)r * (uint32_t)g.K + (uint32_t)(c + 16 * chunk);
+    } else {
+      const int c = min(it.nt * 256 + 64 * i, cols - 64) + (tid >> 3);
+      woff[i] = (uint32_t)c * (uint32_t)g.K + (uint32_t)(((tid & 7) ^ swz_w(tid >> 3)) * 16);
+    }
+  }
+  // (copies that are not wanted, of rows past the tile or steps past the piece,
+  // read an empty buffer: no branches, and every step issues the same number)
+  auto copy_a = [&](int st, bool live, const BigStage& s) {
+    const bool in = TRANS ? st * 128 + acol < red : true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      copy16_to_lds(raw_buffer(g.a, live && 4 * i < blocks ? abytes : 0u),
+                    in ? aoff[i] : 0xFFFFFFF0u - (uint32_t)st * 128u, (uint32_t)st * 128u,
+                    s.a + (512 * i + 64 * wave) * 16);
+  };
+  auto copy_w = [&](int st, bool live, const BigStage& s) {
+    const __amdgpu_buffer_rsrc_t rsrc = raw_buffer(wbase, live ? wbytes : 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TRANS) {
+        // W rows past N lie past the buffer's end
+        copy16_to_lds(rsrc, woff[i] + (uint32_t)st * 128u * (uint32_t)g.K, 0,
+                      s.w + (wave >> 1) * 8192 + (wave & 1) * 4096 + i * 1024);
+      } else {
+        copy16_to_lds(rsrc, woff[i], (uint32_t)st * 128u, s.w + (512 * i + 64 * wave) * 16);
+      }
+    }
+  };
+
+  const int base = it.nt * 256 + nq * 64;
+  const bool active = base < cols;
+  const int cbase = active ? base : cols - 64;
+  const int KB = g.K >> 7;
+  const int64_t sat = TRANS ? (int64_t)it.expert * steps * KB + (cbase >> 7)
+                            : ((int64_t)it.expert * ((g.N + 127) >> 7) + (cbase >> 7)) * steps;
+  const int at = rows_at(i16, q);
+  const int ah = at + half * h0 * 2048;
+  const int tr_row = 64 * (q & 1) + 32 * (q >> 1) + (i16 >> 1);
+  const int tr_at = nq * 8192 + tr_row * 64 + (swz_t(tr_row) << 4) + (i16 & 1) * 8;
+
+  f32x4_t acc[NMB][4];
+#pragma unroll
+  for (int mb = 0; mb < NMB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto read_w = [&](const BigStage& s, WStep& w) {
+    if constexpr (TRANS) {
+      // reduced values 64 (q & 1) + 32 (q / 2) + 8 t .. + 7, columns 16 nb ..:
+      // row r = tr_row + 8 t, chunk nb, whose slot is nb ^ swz_t(r)
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const i32x2_t v = lds_tr8(s.w + ((tr_at ^ (nb << 4)) + t * 512));
+          w.w[nb][2 * t] = v[0];
+          w.w[nb][2 * t + 1] = v[1];
+        }
+    } else {
+      // MFMA row i of block nb is column 16 (i / 4) + 4 nb + (i & 3)
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        const int r = nq * 64 + 16 * (i16 >> 2) + 4 * nb + (i16 & 3);
+        const int o = r * 128 + (((4 * (q & 1) + 2 * (q >> 1)) ^ swz_w(r)) << 4);
+        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(s.w + o);
+        const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(s.w + (o ^ 16));
+        w.w[nb] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                          (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+      }
+    }
+  };
+  // Step i of n from stage s, rows of step i + 1 to stage t.  Once every
+  // wavefront holds its weights in registers their stage is free, so the
+  // weights of step i + 2 (which come from memory) start two steps ahead of
+  // their use, the rows (which the L2 mostly holds) one.
+  auto step = [&](int st0, int i, int n, const BigStage& s, const BigStage& t) {
+    copy_a(st0 + i + 1, i + 1 < n, t);
+    WStep w;
+    read_w(s, w);
+    stage_barrier<63>();
+    copy_w(st0 + i + 2, i + 2 < n, s);
+    int xs[2];
+    const uint2 v = *reinterpret_cast<const uint2*>(sc + ((i * 2 + half) * 16 + i16) * 8);
+    xs[0] = (int)v.x;
+    xs[1] = (int)v.y;
+    mfma_step<WF32, NMB>(s.a, w, wt[nq * kPiece + i], xs, ah, acc);
+    stage_barrier<4>();
+  };
+
+  for (int st0 = 0; st0 < steps; st0 += kPiece) {
+    const int n = min(kPiece, steps - st0);
+    copy_a(st0, true, s0);
+    copy_w(st0, true, s0);
+    copy_w(st0 + 1, n > 1, s1);
+    // scales: sc[step][half][row & 15][block of the half], wt[column group][step]
+    for (int v = tid; v < 32 * blocks; v += 512) {
+      const int r = v >> 1, b = r >> 4, hb = b >= h0;
+      const int rr = it.row0 + (r < it.nrows ? r : 0);
+      const int64_t src = g.tokens ? g.perm[rr] / g.topk : rr;
+      const uint8_t* row = g.a_scales + src * steps + st0;
+      uint8_t* out = sc + (hb * 16 + (r & 15)) * 8 + (b - hb * h0);
+#pragma unroll 8
+      for (int j = v & 1; j < n; j += 2) out[j * 256] = row[j];
+    }
+    if (half == 0)
+      for (int j = lane; j < n; j += 64) {
+        const int64_t si = sat + (int64_t)(st0 + j) * (TRANS ? KB : 1);
+        wt[nq * kPiece + j] = WF32 ? static_cast<const uint32_t*>(g.w_scales)[si]
+                                   : static_cast<const uint8_t*>(g.w_scales)[si];
+      }
+    stage_barrier<0>();
+#pragma nounroll
+    for (int i = 0; i < n; i += 2) {
+      step(st0, i, n, s0, s1);
+      if (i + 1 >= n) break;
+      step(st0, i + 1, n, s1, s0);
+    }
+    stage_barrier<0>();
+  }
+  if (!active) return;
+#pragma unroll
+  for (int mb = 0; mb < NMB; ++mb) {
+    const int r = 16 * (half * h0 + mb) + i16;
+    if (r >= it.nrows || (half == 0 && mb >= h0)) continue;
+    uint16_t* out = g.y + (int64_t)(it.row0 + r) * cols + cbase;
+    if constexpr (TRANS) {
+      // block nb holds columns 16 nb + 4 q .. + 3
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb)
+        *reinterpret_cast<uint2*>(out + 16 * nb + 4 * q) =
+            make_uint2(pack_bf16x2(acc[mb][nb][0], acc[mb][nb][1]),
+                       pack_bf16x2(acc[mb][nb][2], acc[mb][nb][3]));
+    } else {
+      // block nb holds columns 16 q + 4 nb .. + 3
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4_t*>(out + 16 * q + 8 * h) =
+            u32x4_t{pack_bf16x2(acc[mb][2 * h][0], acc[mb][2 * h][1]),
+                    pack_bf16x2(acc[mb][2 * h][2], acc[mb][2 * h][3]),
+                    pack_bf16x2(acc[mb][2 * h + 1][0], acc[mb][2 * h + 1][1]),
+                    pack_bf16x2(acc[mb][2 * h + 1][2], acc[mb][2 * h + 1][3])};
+    }
+  }
+}
+
+template <bool TRANS, bool WF32>
+__global__ __launch_bounds__(512, 1) void k_fp8_gemm_big(Fp8GemmArgs g, int ntn) {
+  __shared__ __attribute__((aligned(16))) uint8_t a0[32768];
+  __shared__ __attribute__((aligned(16))) uint8_t a1[32768];
+  __shared__ __attribute__((aligned(16))) uint8_t w0[32768];
+  __shared__ __attribute__((aligned(16))) uint8_t w1[32768];
+  __shared__ __attribute__((aligned(16))) uint8_t sc[kPiece * 256];
+  __shared__ uint32_t wt[4 * kPiece];
+  __shared__ int tiles_before[1025];
+  __shared__ int scratch[16];
+  __shared__ int item[4];
+  const BigStage s0{a0, w0}, s1{a1, w1};
+  count_tiles(g.counts, g.E, 256, tiles_before, scratch);
+  const int items = tiles_before[g.E] * ntn;
+  const int per = (items + 7) >> 3;
+  const int first = (blockIdx.x & 7) * per, last = min(first + per, items);
+  for (int i = first + (blockIdx.x >> 3); i < last; i += gridDim.x >> 3) {
+    __syncthreads();
+    find_item(i, ntn, tiles_before, g.counts, g.offsets, g.E, item);
+    __syncthreads();
+    Item it;
+    it.expert = __builtin_amdgcn_readfirstlane(item[0]);
+    it.row0 = __builtin_amdgcn_readfirstlane(item[1]);
+    it.nrows = __builtin_amdgcn_readfirstlane(item[2]);
+    it.nt = __builtin_amdgcn_readfirstlane(item[3]);
+    const int h0 = (((it.nrows + 15) >> 4) + 1) >> 1;
+    auto run = [&](auto n) {
+      big_item<TRANS, WF32, decltype(n)::value>(g, it, s0, s1, sc, wt);
+    };
+    using std::integral_constant;
+    if (h0 > 6) run(integral_constant<int, 8>{});
+    else if (h0 > 5) run(integral_constant<int, 6>{});
+    else if (h0 > 4) run(integral_constant<int, 5>{});
+    else if (h0 > 2) run(integral_constant<int, 4>{});
+    else run(integral_constant<int, 2>{});
   }
 }
 
@@ -500,25 +782,21 @@ int tile_blocks(const Fp8GemmArgs& g) {
 
 }  // namespace
 
-template <bool TRANS, bool WF32, int MB, int NB>
-static void launch(const Fp8GemmArgs& g, int64_t tiles, hipStream_t s) {
-  const int ntn = ((TRANS ? g.K : g.N) + 64 * NB - 1) / (64 * NB);
-  // a multiple of 8: one stretch of items per XCD
-  const int64_t resident = (int64_t)num_cus() / 8 * 8 * (NB == 8 ? 1 : 2);
-  const int64_t grid = std::min<int64_t>((tiles * ntn + 7) / 8 * 8, resident);
-  hipLaunchKernelGGL((k_fp8_gemm<TRANS, WF32, MB, NB>), dim3((unsigned)grid), dim3(256), 0, s, g,
-                     ntn);
-}
-
 template <bool TRANS, bool WF32>
 static void launch_sized(const Fp8GemmArgs& g, hipStream_t s) {
   const int mb = tile_blocks(g);
-  const char* xx = getenv("QGG_X");
-  const int64_t tiles = std::min<int64_t>(g.P, g.P / (16 * mb) + g.E);
-  if (mb == 2) launch<TRANS, WF32, 2, 4>(g, tiles, s);
-  else if (mb == 4) launch<TRANS, WF32, 4, 4>(g, tiles, s);
-  else if (TRANS || WF32 || xx || tiles * (g.N / 512) < num_cus()) launch<TRANS, WF32, 8, 4>(g, tiles, s);
-  else launch<false, false, 8, 8>(g, tiles, s);
+  const int mt = mb == 8 ? 256 : 16 * mb;
+  const int64_t tiles = std::min<int64_t>(g.P, g.P / mt + g.E);
+  const int ntn = ((TRANS ? g.K : g.N) + 255) / 256;
+  // a multiple of 8: one stretch of items per XCD
+  const int64_t items = (tiles * ntn + 7) / 8 * 8, cus = num_cus() / 8 * 8;
+  const dim3 grid((unsigned)std::min<int64_t>(items, mb == 8 ? cus : 2 * cus));
+  if (mb == 8)
+    hipLaunchKernelGGL((k_fp8_gemm_big<TRANS, WF32>), grid, dim3(512), 0, s, g, ntn);
+  else if (mb == 4)
+    hipLaunchKernelGGL((k_fp8_gemm<TRANS, WF32, 4>), grid, dim3(256), 0, s, g, ntn);
+  else
+    hipLaunchKernelGGL((k_fp8_gemm<TRANS, WF32, 2>), grid, dim3(256), 0, s, g, ntn);
 }
 
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& g, hipStream_t s) {

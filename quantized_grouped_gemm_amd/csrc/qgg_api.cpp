@@ -945,8 +945,8 @@ qgg_status fp8_grouped_gemm(const qgg_fp8_weight* w, const uint8_t* a, const uin
   const bool trans = flags & QGG_TRANSPOSE_W, tokens = flags & QGG_A_TOKENS;
   const int red = trans ? w->N : w->K;
   const int64_t rows = tokens ? T : P;
-  constexpr int64_t kMost = 0xFFFFFFF0;          // 32-bit buffer offsets, the top 16 kept for "outside"
-  if (red > kMaxReduced || rows * red >= kMost || (int64_t)w->N * w->K >= kMost)
+  constexpr int64_t kMost = 0xFFFF0000;          // 32-bit buffer offsets, the top kept for "outside"
+  if (red > kMaxReduced || rows * red >= kMost || (int64_t)(w->N + 64) * w->K >= kMost)
     return QGG_ERR_UNSUPPORTED;
   if (P == 0) return QGG_OK;
   Fp8GemmArgs g;
