@@ -306,6 +306,17 @@ def test_quantize_every_scale_and_every_code():
         np.testing.assert_array_equal(value(c, s), x.double().numpy())
 
 
+def test_dequantize_every_scale():
+    """Every scale byte: 2^(c - 127), rounded once to BF16 with the code; 255 is NaN."""
+    codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8).view(256, 1).repeat(1, 2).contiguous()
+    back = qgg.fp8_dequantize(codes.to(DEV), scales.to(DEV)).cpu()
+    s = np.exp2(np.arange(256) - 127.0)
+    s[255] = np.nan
+    want = codes.view(torch.float8_e4m3fn).double() * torch.from_numpy(s)[:, None]
+    np.testing.assert_array_equal(back.double().numpy(), want.to(torch.bfloat16).double().numpy())
+
+
 def test_rows_past_32_bit_offsets():
     M, C = 600_000, 7168                    # 4.3e9 values
     x = torch.empty((M, C), dtype=torch.bfloat16, device=DEV)
@@ -337,11 +348,20 @@ def check_rows(got, want, slack):
         assert np.all(lo[live] <= 448 * s[live, b]) and np.all((hi[live] > 224 * s[live, b]) | (s[live, b] == 2.0 ** -127))
 
 
+def check_exact(got, want):
+    """8-bit rows that are those of the 64-bit values: the same scales and codes.  A 64-bit value carries a few times 2^-53,
+    and may round another way where it is that near to a border: one value in 2^53 / 2^6, so none is let off."""
+    q, s = quantize64(want)
+    np.testing.assert_array_equal(got[1].cpu().double().numpy(), s)
+    np.testing.assert_array_equal(got[0].cpu().double().numpy(), q)
+
+
 def swiglu64(h):
     h = h.double().numpy()
     I = h.shape[1] // 2
     g, u = h[:, :I], h[:, I:]
-    return g * 1 / (1 + np.exp(-g)) * u
+    with np.errstate(over="ignore"):
+        return g * 1 / (1 + np.exp(-g)) * u
 
 
 # exp (2 steps, argument up to 90: 90 more near the ends, where the value is as good as 0 or 1), division 2, products 2
@@ -363,6 +383,7 @@ def test_swiglu_fp8(P, inter):
     a = r["a"].cpu().double().numpy()
     assert np.all(np.abs(a - ref) <= HBF * np.abs(ref) + 1.01 * slack)
     check_rows((r["a8"], r["a8_scales"]), ref, slack)
+    check_exact((r["a8"], r["a8_scales"]), ref)
     q, s = quantize64(h.double().numpy())
     np.testing.assert_array_equal(r["h8"].cpu().double().numpy(), q)
     np.testing.assert_array_equal(r["h8_scales"].cpu().double().numpy(), s)
@@ -370,6 +391,27 @@ def test_swiglu_fp8(P, inter):
     for name in ("a", "a8", "h8"):
         one = qgg.swiglu_fp8(h.to(DEV), want=(name,))
         assert torch.equal(one[name].view(torch.uint8), r[name].view(torch.uint8))
+
+
+def test_swiglu_codes_of_many_rows():
+    """4 million values, far and near: fp32 arithmetic alone would get some tens of codes wrong."""
+    h = normal(gen(99), 1024, 8192, std=3.0)
+    h[::7] *= 8
+    h[5::31, ::3] = -100
+    r = qgg.swiglu_fp8(h.to(DEV), want=("a8",))
+    check_exact((r["a8"], r["a8_scales"]), swiglu64(h))
+
+
+def test_swiglu_values_that_are_not_finite():
+    h = normal(gen(6), 4, 512)
+    h[0, 3], h[1, 300], h[2, 5], h[3, 7] = float("nan"), float("inf"), float("-inf"), float("inf")
+    r = qgg.swiglu_fp8(h.to(DEV))
+    fine = normal(gen(6), 4, 512)
+    want = torch.from_numpy(swiglu64(fine))
+    for i, c in ((0, 3), (1, 44), (2, 5), (3, 7)):
+        assert torch.isnan(r["a8"][i, c].float())
+        want[i, c] = float("nan")
+    check_exact((r["a8"], r["a8_scales"]), want.numpy())
 
 
 def perm_of(ids, E):
@@ -414,6 +456,7 @@ def test_swiglu_fp8_bwd(T, k, inter, drop):
     got = r["dh"].cpu().double().numpy()
     assert np.all(np.abs(got - dh)[:live] <= (HBF * np.abs(dh) + 1.01 * slack)[:live])
     check_rows((r["dh8"][:live], r["dh8_scales"][:live]), dh[:live], slack[:live])
+    check_exact((r["dh8"][:live], r["dh8_scales"][:live]), dh[:live])
     # a sum of `inter` terms in fp32: a lane adds inter / 32, then 8 levels
     tol = np.zeros(P)
     perm = p.perm.cpu().numpy()[:live]
