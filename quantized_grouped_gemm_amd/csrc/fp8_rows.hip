@@ -44,6 +44,22 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return v;
 }
 
+// Sum over the wavefront, in lane 63 (a fixed order).
+__device__ __forceinline__ float wave_sum_63(float v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(
+        0, __float_as_int(v), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});    // quad_perm 1,0,3,2
+  add(integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});    // quad_perm 2,3,0,1
+  add(integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});   // row_half_mirror
+  add(integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});   // row_mirror
+  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // row_bcast:15
+  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});   // row_bcast:31
+  return v;
+}
+
 typedef short s16x2_t __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
 
@@ -140,7 +156,11 @@ __device__ __forceinline__ float round_to_odd(double x) {
 typedef float f32x8_t __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ float pick(const float v[8], int i) {
   const f32x8_t x = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
-  return x[i];
+  float e = x[i];
+  // pins what follows from it to its place: the double arithmetic of two rare
+  // paths would otherwise be shared, and computed before either is entered
+  asm volatile("" : "+v"(e));
+  return e;
 }
 
 // Codes of eight values that are known to lie between lo[i] and hi[i], as those
@@ -154,16 +174,20 @@ __device__ __forceinline__ float pick(const float v[8], int i) {
 // that are not finite) the whole block is taken exactly.
 constexpr float kMargin = 0x1p-15f;
 
-template <typename Exact>
-__device__ __forceinline__ uint2 quantize8_exact(const float lo[8], const float hi[8], Exact exact,
-                                                 int* code) {
+// HI: |hi| >= |lo|.  `all`: a lane has a value that lo and hi do not hold.
+template <bool HI, typename Exact>
+__device__ __forceinline__ uint2 quantize8_exact(const float lo[8], const float hi[8], bool all,
+                                                 Exact exact, int* code) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, max(mag_bits(lo[i]), mag_bits(hi[i])));
+  for (int i = 0; i < 8; ++i) {
+    top = max(top, mag_bits(hi[i]));
+    if (!HI) top = max(top, mag_bits(lo[i]));
+  }
   top = row16_max(top);
   *code = block_scale(top);
   const float low = __uint_as_float(top) * (1.0f - kMargin);
-  if (__any(top >= kInfBits || block_scale(mag_bits(low)) != *code)) {
+  if (__any(all || top >= kInfBits || block_scale(mag_bits(low)) != *code)) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = exact(i);
@@ -258,14 +282,20 @@ __device__ __forceinline__ void sigmoid2(float z, float* f, float* one_minus_f) 
 }
 constexpr float kHalfStep = 0x1p-24f;
 
-// The same in fewer operations for z >= -80 (half steps: f |z| + 6, 1 - f one
-// more than twice the exponential's share: 2 |z| + 9); below, the values of
-// -80, which bound the true ones.
-constexpr float kFar = -80.0f;
+// The same in fewer operations for z >= kFar (half steps: f |z| + 6, 1 - f |z|
+// + 9), where exp(-z) and f are normal numbers.
+constexpr float kFar = -87.0f;
 __device__ __forceinline__ void sigmoid2_near(float z, float* f, float* one_minus_f) {
-  const float e = __expf(-fmaxf(z, kFar));
+  const float e = __expf(-z);
   *f = __builtin_amdgcn_rcpf(1.0f + e);
   *one_minus_f = e * *f;
+}
+
+__device__ __forceinline__ bool any_far(const float z[8]) {
+  bool far = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) far |= z[i] < kFar;
+  return far;
 }
 
 __device__ __forceinline__ double sigmoid64(double z) { return 1.0 / (1.0 + exp(-z)); }
@@ -319,7 +349,7 @@ __global__ __launch_bounds__(256) void k_swiglu_fp8(const uint16_t* __restrict__
         sigmoid2_near(g[i], &f, &f1);
         const float v = g[i] * f * u[i];
         // half steps: f and two products
-        const float w = g[i] < kFar ? 1.0f : __builtin_fmaf(fabsf(g[i]), kHalfStep, 9 * kHalfStep);
+        const float w = __builtin_fmaf(fabsf(g[i]), kHalfStep, 9 * kHalfStep);
         lo[i] = __builtin_fmaf(-w, v, v);
         hi[i] = __builtin_fmaf(w, v, v);
       }
@@ -327,7 +357,8 @@ __global__ __launch_bounds__(256) void k_swiglu_fp8(const uint16_t* __restrict__
         const double z = pick(g, i);
         return round_to_odd(z * sigmoid64(z) * (double)pick(u, i));
       };
-      *reinterpret_cast<uint2*>(a8 + r * inter + c) = quantize8_exact(lo, hi, exact, &code);
+      *reinterpret_cast<uint2*>(a8 + r * inter + c) =
+          quantize8_exact<true>(lo, hi, any_far(g), exact, &code);
       if (l == 0) a_scales[r * nb + blk] = (uint8_t)code;
     }
   }
@@ -387,16 +418,16 @@ __global__ __launch_bounds__(256) void k_swiglu_fp8_bwd(
       }
       if constexpr (W & 2) {
         float lo[8], hi[8];
+        const bool far = any_far(g);
         int code;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float f, f1;
           sigmoid2_near(g[i], &f, &f1);
-          // half steps: f |z| + 6; m = 1 + z (1 - f) with 2 |z| + 11 of |z (1
-          // - f)| <= |m| + 1 and its own rounding; four products
+          // half steps: f |z| + 6; m = 1 + z (1 - f) with |z| + 10 of |z (1 -
+          // f)| <= |m| + 1 and its own rounding; four products: of |m| + 1
           const float m = __builtin_fmaf(g[i], f1, 1.0f);
-          const float w = g[i] < kFar ? 1.0f
-                                      : __builtin_fmaf(fabsf(g[i]), 3 * kHalfStep, 24 * kHalfStep);
+          const float w = __builtin_fmaf(fabsf(g[i]), 2 * kHalfStep, 22 * kHalfStep);
           const float slope = gp * d[i] * u[i] * f;
           const float em = __builtin_fmaf(w, fabsf(m), w);
           lo[i] = slope * (m - em);
@@ -407,14 +438,14 @@ __global__ __launch_bounds__(256) void k_swiglu_fp8_bwd(
           return round_to_odd((double)gp * pick(d, i) * pick(u, i) * sigmoid64(z) *
                               (1.0 + z * sigmoid64(-z)));
         };
-        *reinterpret_cast<uint2*>(dh8 + at) = quantize8_exact(lo, hi, exact_g, &code);
+        *reinterpret_cast<uint2*>(dh8 + at) =
+            quantize8_exact<false>(lo, hi, far, exact_g, &code);
         if (l == 0) dh_scales[r * 2 * nb + blk] = (uint8_t)code;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float f, f1;
           sigmoid2_near(g[i], &f, &f1);
-          const float w = g[i] < kFar ? 1.0f
-                                      : __builtin_fmaf(fabsf(g[i]), 3 * kHalfStep, 24 * kHalfStep);
+          const float w = __builtin_fmaf(fabsf(g[i]), 2 * kHalfStep, 22 * kHalfStep);
           const float v = gp * d[i] * (g[i] * f);
           lo[i] = __builtin_fmaf(-w, v, v);
           hi[i] = __builtin_fmaf(w, v, v);
@@ -423,16 +454,16 @@ __global__ __launch_bounds__(256) void k_swiglu_fp8_bwd(
           const double z = pick(g, i);
           return round_to_odd((double)gp * pick(d, i) * z * sigmoid64(z));
         };
-        *reinterpret_cast<uint2*>(dh8 + at + inter) = quantize8_exact(lo, hi, exact_u, &code);
+        *reinterpret_cast<uint2*>(dh8 + at + inter) =
+            quantize8_exact<true>(lo, hi, far, exact_u, &code);
         if (l == 0) dh_scales[r * 2 * nb + nb + blk] = (uint8_t)code;
       }
     }
     if constexpr (W & 4) {
-#pragma unroll
-      for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+      sum = wave_sum_63(sum);
       // two sets of partial sums: the next pair's writes meet the last reads of
       // the one before only after another barrier
-      if ((threadIdx.x & 63) == 0) part[flip][threadIdx.x >> 6] = sum;
+      if ((threadIdx.x & 63) == 63) part[flip][threadIdx.x >> 6] = sum;
       __syncthreads();
       if (threadIdx.x == 0)
         dgates[p] = (part[flip][0] + part[flip][1]) + (part[flip][2] + part[flip][3]);
@@ -444,6 +475,7 @@ __global__ __launch_bounds__(256) void k_swiglu_fp8_bwd(
 // Workgroups of 256 for this many threads; the kernels stride over the rest
 // (a launch holds fewer than 2^32 threads).
 constexpr int64_t kMostGroups = 1 << 22;
+constexpr int kRowGroups = 32;
 unsigned groups(int64_t threads) {
   return (unsigned)std::min<int64_t>((threads + 255) / 256, kMostGroups);
 }
@@ -487,7 +519,7 @@ hipError_t launch_swiglu_fp8_bwd(const uint16_t* da, const uint8_t* h8, const ui
                                  hipStream_t s) {
   TimedLaunch timed_(kLOther, s);
   if (P == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>(P, kMostGroups));
+  const dim3 grid((unsigned)std::min<int64_t>(P, (int64_t)num_cus() * kRowGroups));
   auto go = [&](auto w) {
     hipLaunchKernelGGL(k_swiglu_fp8_bwd<decltype(w)::value>, grid, dim3(256), 0, s, da, h8,
                        h_scales, gates, inv_perm, P, inter, dh, dh8, dh_scales, dgates);
