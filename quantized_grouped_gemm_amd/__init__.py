@@ -612,21 +612,30 @@ def _need(name: str, t, dtypes, shape=None, device=None):
 
 
 class _On:
-    """Makes a tensor's device current for a call (launches go to the current device)."""
+    """Makes a tensor's device current for a call (launches go to the current device) and gives
+    that device's current stream.  The stream handle is read without a Stream object around it,
+    whose making costs as much as a launch."""
 
     def __init__(self, device):
         import torch
+        self.index = device.index
         self.guard = None
-        if device.index != torch.cuda.current_device():
+        if self.index != torch._C._cuda_getDevice():
             self.guard = torch.cuda.device(device)
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
+        return self.raw_stream(self.index)
 
     def __exit__(self, *a):
         if self.guard is not None:
             self.guard.__exit__(*a)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need_perm(perm: Perm, P: int, device, E: int | None = None):
@@ -671,12 +680,12 @@ def moe_route_scored(logits, k: int, score: str = "sigmoid", bias=None, n_group:
     if n_group == 1:
         group_top = 1
     o = _route_opts(score, n_group, topk_group, group_top, renorm, scale)
-    with _On(dev):
+    with _On(dev) as stream:
         ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
         gates = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-        _check(lib().moe_route_scored(_ptr(logits), int(logits.dtype == torch.bfloat16),
-                                      _ptr(bias), T, E, k, ctypes.byref(o), _ptr(ids), _ptr(gates),
-                                      _ptr(err_flag), _stream()), "moe_route_scored")
+        _check(lib().moe_route_scored(_at(logits), int(logits.dtype == torch.bfloat16),
+                                      _at(bias), T, E, k, ctypes.byref(o), _at(ids), _at(gates),
+                                      _at(err_flag), stream), "moe_route_scored")
     return ids, gates
 
 
@@ -691,11 +700,11 @@ def moe_route_scored_bwd(logits, topk_ids, dgates, score: str = "sigmoid", renor
     k = topk_ids.shape[1]
     _need("dgates", dgates, (torch.float32,), (T, k), dev)
     o = _route_opts(score, 1, 1, 1, renorm, scale)
-    with _On(dev):
+    with _On(dev) as stream:
         dl = torch.empty_like(logits)
-        _check(lib().moe_route_scored_bwd(_ptr(logits), int(logits.dtype == torch.bfloat16),
-                                          _ptr(topk_ids), _ptr(dgates), T, E, k, ctypes.byref(o),
-                                          _ptr(dl), _stream()), "moe_route_scored_bwd")
+        _check(lib().moe_route_scored_bwd(_at(logits), int(logits.dtype == torch.bfloat16),
+                                          _at(topk_ids), _at(dgates), T, E, k, ctypes.byref(o),
+                                          _at(dl), stream), "moe_route_scored_bwd")
     return dl
 
 
@@ -704,11 +713,11 @@ def fp8_quantize(x):
     import torch
     _need("x", x, (torch.bfloat16,), (-1, -1))
     M, C = x.shape
-    with _On(x.device):
+    with _On(x.device) as stream:
         codes = torch.empty((M, C), dtype=torch.float8_e4m3fn, device=x.device)
         scales = torch.empty((M, -(-C // SCALE_BLOCK)), dtype=torch.float8_e8m0fnu,
                              device=x.device)
-        _check(lib().qgg_fp8_quantize(_ptr(x), M, C, _ptr(codes), _ptr(scales), _stream()),
+        _check(lib().qgg_fp8_quantize(_at(x), M, C, _at(codes), _at(scales), stream),
                "qgg_fp8_quantize")
     return codes, scales
 
@@ -720,9 +729,9 @@ def fp8_dequantize(codes, scales):
     _need("codes", codes, ct, (-1, -1))
     M, C = codes.shape
     _need("scales", scales, st, (M, -(-C // SCALE_BLOCK)), codes.device)
-    with _On(codes.device):
+    with _On(codes.device) as stream:
         x = torch.empty((M, C), dtype=torch.bfloat16, device=codes.device)
-        _check(lib().qgg_fp8_dequantize(_ptr(codes), _ptr(scales), M, C, _ptr(x), _stream()),
+        _check(lib().qgg_fp8_dequantize(_at(codes), _at(scales), M, C, _at(x), stream),
                "qgg_fp8_dequantize")
     return x
 
@@ -778,11 +787,11 @@ def fp8_grouped_gemm(w: Fp8Weight, a, a_scales, perm: Perm, T: int, k: int, flag
     _need_perm(perm, P, dev, w.E)
     if out is not None:
         _need("out", out, (torch.bfloat16,), (P, cols), dev)
-    with _On(dev):
+    with _On(dev) as stream:
         y = out if out is not None else torch.empty((P, cols), dtype=torch.bfloat16, device=dev)
         wc, pc = w.c(), perm.c()
-        _check(lib().fp8_grouped_gemm(ctypes.byref(wc), _ptr(a), _ptr(a_scales), flags,
-                                      ctypes.byref(pc), T, k, _ptr(y), _stream()),
+        _check(lib().fp8_grouped_gemm(ctypes.byref(wc), _at(a), _at(a_scales), flags,
+                                      ctypes.byref(pc), T, k, _at(y), stream),
                "fp8_grouped_gemm")
     return y
 
@@ -802,7 +811,7 @@ def swiglu_fp8(h, perm: Perm | None = None, want=("a8", "h8")):
         _need_perm(perm, P, dev)
     nb = -(-inter // SCALE_BLOCK)
     r = dict.fromkeys(("a", "a8", "a8_scales", "h8", "h8_scales"))
-    with _On(dev):
+    with _On(dev) as stream:
         if "a" in want:
             r["a"] = torch.empty((P, inter), dtype=torch.bfloat16, device=dev)
         for name, n in (("a8", 1), ("h8", 2)):
@@ -812,9 +821,9 @@ def swiglu_fp8(h, perm: Perm | None = None, want=("a8", "h8")):
                                                   device=dev)
         live = None if perm is None else ctypes.c_void_p(
             perm.offsets.data_ptr() + 4 * (perm.offsets.numel() - 1))
-        _check(lib().moe_swiglu_fp8(_ptr(h), live, P, inter, _ptr(r["a"]), _ptr(r["a8"]),
-                                    _ptr(r["a8_scales"]), _ptr(r["h8"]), _ptr(r["h8_scales"]),
-                                    _stream()), "moe_swiglu_fp8")
+        _check(lib().moe_swiglu_fp8(_at(h), live, P, inter, _at(r["a"]), _at(r["a8"]),
+                                    _at(r["a8_scales"]), _at(r["h8"]), _at(r["h8_scales"]),
+                                    stream), "moe_swiglu_fp8")
     return r
 
 
@@ -837,7 +846,7 @@ def swiglu_fp8_bwd(da, h8, h8_scales, topk_gates, perm: Perm, want=("dh8", "dgat
     if not set(want) <= {"dh", "dh8", "dgates"}:
         raise QggError(f"want: {want}")
     r = dict.fromkeys(("dh", "dh8", "dh8_scales", "dgates"))
-    with _On(dev):
+    with _On(dev) as stream:
         if "dh" in want:
             r["dh"] = torch.empty((P, 2 * inter), dtype=torch.bfloat16, device=dev)
         if "dh8" in want:
@@ -846,10 +855,10 @@ def swiglu_fp8_bwd(da, h8, h8_scales, topk_gates, perm: Perm, want=("dh8", "dgat
         if "dgates" in want:
             r["dgates"] = torch.empty((T, k), dtype=torch.float32, device=dev)
         pc = perm.c()
-        _check(lib().moe_swiglu_fp8_bwd(_ptr(da), _ptr(h8), _ptr(h8_scales), _ptr(topk_gates),
-                                        ctypes.byref(pc), T, k, inter, _ptr(r["dh"]),
-                                        _ptr(r["dh8"]), _ptr(r["dh8_scales"]), _ptr(r["dgates"]),
-                                        _stream()), "moe_swiglu_fp8_bwd")
+        _check(lib().moe_swiglu_fp8_bwd(_at(da), _at(h8), _at(h8_scales), _at(topk_gates),
+                                        ctypes.byref(pc), T, k, inter, _at(r["dh"]),
+                                        _at(r["dh8"]), _at(r["dh8_scales"]), _at(r["dgates"]),
+                                        stream), "moe_swiglu_fp8_bwd")
     return r
 
 
@@ -863,9 +872,9 @@ def moe_combine(rows, perm: Perm, T: int, k: int, topk_gates=None):
     if topk_gates is not None:
         _need("topk_gates", topk_gates, (torch.float32,), (T, k), dev)
     d = rows.shape[1]
-    with _On(dev):
+    with _On(dev) as stream:
         y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
         pc = perm.c()
-        _check(lib().moe_combine(_ptr(rows), d, ctypes.byref(pc), _ptr(topk_gates), T, k, _ptr(y),
-                                 _stream()), "moe_combine")
+        _check(lib().moe_combine(_at(rows), d, ctypes.byref(pc), _at(topk_gates), T, k, _at(y),
+                                 stream), "moe_combine")
     return y

@@ -8,9 +8,14 @@
 //   largest groups stay (equal scores: lower group first)
 //   the k largest c of the kept groups, equal values in ascending id
 //   w_j = s[id_j], divided by their sum when renorm, times scale.
-// Scores and choice values are formed in double: a choice is a comparison of
-// nearby numbers, and rounding s to 24 bits would turn near values into ties
-// or swap them (about two tokens in a batch of 8192 with 256 experts).
+// The choice is that of scores and choice values in double: it compares nearby
+// numbers, and in 24 bits near values become ties or swap (about two tokens in
+// a batch of 8192 with 256 experts).  Few comparisons need that, though, so a
+// token is first decided in fp32, by the logits themselves where no bias enters
+// (both scores grow with them) and else by fp32 choice values; where two
+// neighbours of the order, the last kept and the first dropped, or two groups
+// lie closer than the error of what was compared, the token is decided again
+// in double.
 #include "qgg_device.hpp"
 #include "qgg_internal.hpp"
 
@@ -55,6 +60,279 @@ __device__ __forceinline__ double read_lane_f64(double v, int lane) {
   return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  auto step = [&](auto ctrl, auto rows) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value,
+                                                     decltype(rows)::value, 0xF, false));
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});   // quad_perm 1,0,3,2
+  step(integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});   // quad_perm 2,3,0,1
+  step(integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});  // row_half_mirror
+  step(integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});  // row_mirror
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast:15
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast:31
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+__device__ __forceinline__ float read_lane_f32(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Layout of the groups over a wavefront: 2^sh lanes each, the largest power of
+// two that gives every group its lanes.
+__device__ __forceinline__ int group_shift(int n_group) {
+  int sh = 0;
+  while ((n_group << (sh + 1)) <= 64) ++sh;
+  return sh;
+}
+
+// A token's choice: lane j < k holds the id and the logit of its j-th expert.
+struct Pick {
+  int id;
+  float l;
+};
+
+// k rounds of a wavefront arg-max over the lanes' keys (0: no candidate); among
+// equal keys the lowest id.  MaxKey is the maximum over the wavefront, `each`
+// gets every round's key in order, and the next one's after the last round.
+template <int NV, typename K, typename MaxKey, typename Each>
+__device__ __forceinline__ Pick take(K (&key)[NV], const float (&l)[NV], int k, int lane,
+                                     MaxKey max_key, Each each) {
+  K best = 0;
+  int best_i = 0;
+  float best_l = 0.f;
+  auto lane_best = [&]() {
+    best = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        best_i = i;
+        best_l = l[i];
+      }
+  };
+  lane_best();
+  Pick p{0, -INFINITY};
+  for (int j = 0; j < k; ++j) {
+    const K top = max_key(best);
+    each(j, top);
+    uint64_t holders = __ballot(best == top);
+    int win = __ffsll((unsigned long long)holders) - 1;
+    int id = 64 * __builtin_amdgcn_readlane(best_i, win) + win;
+    for (holders &= holders - 1; holders; holders &= holders - 1) {
+      const int h = __ffsll((unsigned long long)holders) - 1;
+      const int hid = 64 * __builtin_amdgcn_readlane(best_i, h) + h;
+      if (hid < id) {
+        id = hid;
+        win = h;
+      }
+    }
+    const float wl = read_lane_f32(best_l, win);
+    if (lane == j) {
+      p.id = id;
+      p.l = wl;
+    }
+    if (lane == win) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i == best_i) key[i] = 0;
+      lane_best();
+    }
+  }
+  each(k, max_key(best));
+  return p;
+}
+
+// Two best of each group from the wavefront's row of choice values: the lane's
+// group holds them in all of its lanes afterwards.
+template <typename F>
+__device__ __forceinline__ void group_best(const F* row, int size, int n_group, int sh, int lane,
+                                           F& b1, F& b2) {
+  const int per = 1 << sh, g = lane >> sh;
+  b1 = b2 = -INFINITY;
+  if (g < n_group)
+    for (int i = lane & (per - 1); i < size; i += per) {
+      const F v = row[g * size + i];
+      b2 = max(b2, min(b1, v));
+      b1 = max(b1, v);
+    }
+  for (int off = 1; off < per; off <<= 1) {
+    const F o1 = __shfl_xor(b1, off, kWave), o2 = __shfl_xor(b2, off, kWave);
+    b2 = max(min(b1, o1), max(b2, o2));
+    b1 = max(b1, o1);
+  }
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) { return read_lane_f32(v, lane); }
+__device__ __forceinline__ double lane_value(double v, int lane) { return read_lane_f64(v, lane); }
+
+// Kept groups as bits g << sh: the topk_group largest scores, the lower group
+// first among equals.
+template <typename F>
+__device__ __forceinline__ uint64_t keep_groups(F score, const RouteOpts& o, int sh, int lane) {
+  const int g = lane >> sh;
+  int rank = 0;
+  for (int j = 0; j < o.n_group; ++j) {
+    const F other = lane_value(score, j << sh);
+    rank += other > score || (other == score && j < g);
+  }
+  return __ballot(rank < o.topk_group && (lane & ((1 << sh) - 1)) == 0 && g < o.n_group);
+}
+
+// The choice in double.
+template <int NV>
+__device__ __forceinline__ Pick choose64(const float (&l)[NV], const float* bias, int E, int k,
+                                         const RouteOpts& o, int lane, double* row) {
+  double c[NV];
+  if (o.softmax) {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
+    m = wave_max_f32(m);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      c[i] = l[i] == -INFINITY ? 0.0 : exp((double)l[i] - (double)m);
+      sum += c[i];
+    }
+    sum = wave_sum_f64(sum);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c[i] = sum > 0.0 ? c[i] / sum : 0.0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+  }
+  uint64_t key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 64 * i;
+    const float b = bias && e < E ? bias[e] : 0.f;
+    c[i] = l[i] == -INFINITY || !__builtin_isfinite(b) ? -INFINITY : c[i] + (double)b;
+    key[i] = e < E ? order_key64(c[i]) : 0;
+  }
+  if (o.topk_group < o.n_group) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane + 64 * i < E) row[lane + 64 * i] = c[i];
+    wave_lds_sync();
+    const int size = E / o.n_group, sh = group_shift(o.n_group);
+    double b1, b2;
+    group_best(row, size, o.n_group, sh, lane, b1, b2);
+    const uint64_t kept = keep_groups(o.group_top == 2 ? b1 + b2 : b1, o, sh, lane);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 64 * i;
+      if (e < E && !((kept >> ((e / size) << sh)) & 1)) key[i] = 0;
+    }
+  }
+  return take<NV>(key, l, k, lane, [](uint64_t v) { return wave_max_u64(v); },
+                  [](int, uint64_t) {});
+}
+
+// The choice in fp32; *sure is false where a comparison that decided lies
+// within its error.  Errors, in absolute terms: a sigmoid is off by (|l| + 6)
+// half steps of e / (1 + e)^2 or of itself, under 8 in all (2^-21); a softmax
+// by |l - max| + 24 half steps of p, under 25 (2^-19); the bias adds half a
+// step of the sum.
+template <int NV>
+__device__ __forceinline__ Pick choose32(const float (&l)[NV], const float* bias, int E, int k,
+                                         const RouteOpts& o, int lane, float* row, bool* sure) {
+  const bool grouped = o.topk_group < o.n_group;
+  const bool by_score = bias || (grouped && o.group_top == 2);
+  const float err = o.softmax ? 0x1p-19f : 0x1p-21f;
+  float x[NV], c[NV];                            // what orders experts; what orders groups
+  float m = -INFINITY;
+  if (o.softmax) {
+    uint32_t mk = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mk = max(mk, order_key(l[i]));
+    m = key_value(wave_max_u32(mk));
+  }
+  if (by_score) {
+    if (o.softmax) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        c[i] = l[i] == -INFINITY ? 0.f : __expf(l[i] - m);
+        sum += c[i];
+      }
+      sum = wave_sum_f32(sum);
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) c[i] *= inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 64 * i;
+      const float b = bias && e < E ? bias[e] : 0.f;
+      c[i] = l[i] == -INFINITY || !__builtin_isfinite(b) ? -INFINITY : c[i] + b;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    x[i] = bias ? c[i] : l[i];
+    if (!by_score) c[i] = l[i];
+  }
+  // Logits order as their scores do in double unless they are so near that the
+  // scores round to one number, or so large or small that the scores do.
+  auto near = [&](float hi, float lo) {          // hi >= lo, both compared as x
+    if (hi == lo) return bias != nullptr && hi != -INFINITY;
+    if (bias) return !(hi - lo > 2.0f * err + 0x1p-22f * fmaxf(fabsf(hi), fabsf(lo)));
+    const float top = o.softmax ? hi - m : hi, low = o.softmax ? lo - m : lo;
+    return !(hi - lo > 1e-9f) || top > 20.0f || (low < -600.0f && lo != -INFINITY);
+  };
+  bool ok = true;
+  uint32_t key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    key[i] = lane + 64 * i < E ? order_key(x[i] + 0.0f) : 0;   // -0 -> +0
+  if (grouped) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane + 64 * i < E) row[lane + 64 * i] = c[i];
+    wave_lds_sync();
+    const int size = E / o.n_group, sh = group_shift(o.n_group);
+    float b1, b2;
+    group_best(row, size, o.n_group, sh, lane, b1, b2);
+    const float score = o.group_top == 2 ? b1 + b2 : b1;
+    const uint64_t kept = keep_groups(score, o, sh, lane);
+    float lo = INFINITY, hi = -INFINITY;         // lowest kept, highest dropped
+    for (int j = 0; j < o.n_group; ++j) {
+      const float v = read_lane_f32(score, j << sh);
+      if ((kept >> (j << sh)) & 1) lo = fminf(lo, v);
+      else hi = fmaxf(hi, v);
+    }
+    if (by_score) ok = lo == hi ? lo == -INFINITY
+                                : lo - hi > 4.0f * err + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi));
+    else ok = !near(lo, hi);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 64 * i;
+      if (e < E && !((kept >> ((e / size) << sh)) & 1)) key[i] = 0;
+    }
+  }
+  float prev = 0.f;
+  const Pick p = take<NV>(key, l, k, lane, [](uint32_t v) { return wave_max_u32(v); },
+                          [&](int j, uint32_t top) {
+                            const float v = key_value(top);
+                            if (j > 0 && top != 0 && near(prev, v)) ok = false;
+                            prev = v;
+                          });
+  // softmax gates are formed from the kept logits alone; where the whole row's
+  // sum would round their scores to zero, the other path says so
+  if (o.softmax && bias && __any(lane < k && p.l - m < -600.0f && p.l != -INFINITY)) ok = false;
+  *sure = ok;
+  return p;
+}
+
 // One wavefront per token; lane l holds experts l, l + 64, ... (NV of them).
 template <int NV, typename L>
 __global__ __launch_bounds__(256) void k_route_scored(const L* __restrict__ logits,
@@ -69,8 +347,8 @@ __global__ __launch_bounds__(256) void k_route_scored(const L* __restrict__ logi
   const int t = blockIdx.x * 4 + wave;
   if (t >= T) return;
   const L* row = logits + (int64_t)t * E;
+  double* mine = row_lds + (int64_t)wave * E;
   float l[NV];
-  double s[NV], c[NV];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -80,132 +358,41 @@ __global__ __launch_bounds__(256) void k_route_scored(const L* __restrict__ logi
       const float x = load_logit(row + e);
       if (__builtin_isfinite(x)) l[i] = x;
       else bad = true;
+      if (err && bias && !__builtin_isfinite(bias[e])) bad = true;
     }
+  }
+  if (err && __any(bad) && lane == 0) atomicOr(err, 1);
+
+  bool sure;
+  Pick p = choose32<NV>(l, bias, E, k, o, lane, reinterpret_cast<float*>(mine), &sure);
+  double m = -INFINITY, total = 0.0;             // softmax: maximum and sum of the row
+  if (!sure) {
+    wave_lds_sync();
+    p = choose64<NV>(l, bias, E, k, o, lane, mine);
   }
   if (o.softmax) {
-    float m = l[0];
+    uint32_t mk = 0;
 #pragma unroll
-    for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
-    m = wave_max_f32(m);
+    for (int i = 0; i < NV; ++i) mk = max(mk, order_key(l[i]));
+    m = (double)key_value(wave_max_u32(mk));
+    if (!o.renorm || !sure) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) total += l[i] == -INFINITY ? 0.0 : exp((double)l[i] - m);
+      total = wave_sum_f64(total);
+    }
+  }
+  double w = 0.0;
+  if (lane < k && p.l != -INFINITY) {
+    w = o.softmax ? exp((double)p.l - m) : 1.0 / (1.0 + exp(-(double)p.l));
+    if (o.softmax && (!o.renorm || !sure)) w /= total;
+  }
+  if (o.renorm) {
     double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      s[i] = l[i] == -INFINITY ? 0.0 : exp((double)l[i] - (double)m);
-      sum += s[i];
-    }
-    sum = wave_sum_f64(sum);
-    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] *= inv;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = l[i] == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(-(double)l[i]));
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 64 * i;
-    c[i] = l[i] == -INFINITY ? -INFINITY : s[i];
-    if (bias && e < E) {
-      const float b = bias[e];
-      if (!__builtin_isfinite(b)) {
-        bad = true;
-        c[i] = -INFINITY;
-      } else {
-        c[i] += (double)b;
-      }
-    }
-  }
-  if (__any(bad) && lane == 0 && err) atomicOr(err, 1);
-
-  uint64_t key[NV];                              // 0: not a candidate
-#pragma unroll
-  for (int i = 0; i < NV; ++i) key[i] = lane + 64 * i < E ? order_key64(c[i]) : 0;
-
-  if (o.topk_group < o.n_group) {
-    double* mine = row_lds + (int64_t)wave * E;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane + 64 * i < E) mine[lane + 64 * i] = c[i];
-    wave_lds_sync();
-    const int size = E / o.n_group;
-    // 2^sh lanes a group: the largest power of two that gives every group its lanes
-    int sh = 0;
-    while ((o.n_group << (sh + 1)) <= 64) ++sh;
-    const int per = 1 << sh;
-    const int g = lane >> sh, sub = lane & (per - 1);
-    double b1 = -INFINITY, b2 = -INFINITY;       // the group's two best
-    if (g < o.n_group)
-      for (int i = sub; i < size; i += per) {
-        const double v = mine[g * size + i];
-        b2 = fmax(b2, fmin(b1, v));
-        b1 = fmax(b1, v);
-      }
-    for (int off = 1; off < per; off <<= 1) {
-      const double o1 = __shfl_xor(b1, off, kWave), o2 = __shfl_xor(b2, off, kWave);
-      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-      b1 = fmax(b1, o1);
-    }
-    const double score = o.group_top == 2 ? b1 + b2 : b1;
-    int rank = 0;
-    for (int j = 0; j < o.n_group; ++j) {
-      const double other = read_lane_f64(score, j << sh);
-      rank += other > score || (other == score && j < g);
-    }
-    const uint64_t kept = __ballot(rank < o.topk_group && sub == 0 && g < o.n_group);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E && !((kept >> ((e / size) << sh)) & 1)) key[i] = 0;
-    }
-  }
-
-  // k rounds of a wavefront arg-max; among equal values the lowest id
-  uint64_t best = 0;
-  int best_i = 0;
-  double best_s = 0.0;
-  auto lane_best = [&]() {
-    best = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        best_i = i;
-        best_s = s[i];
-      }
-  };
-  lane_best();
-  int my_id = 0;
-  double my_w = 0.0, sum = 0.0;
-  for (int j = 0; j < k; ++j) {
-    const uint64_t top = wave_max_u64(best);
-    uint64_t holders = __ballot(best == top);
-    int win = __ffsll((unsigned long long)holders) - 1;
-    int id = 64 * __builtin_amdgcn_readlane(best_i, win) + win;
-    for (holders &= holders - 1; holders; holders &= holders - 1) {
-      const int h = __ffsll((unsigned long long)holders) - 1;
-      const int hid = 64 * __builtin_amdgcn_readlane(best_i, h) + h;
-      if (hid < id) {
-        id = hid;
-        win = h;
-      }
-    }
-    const double w = read_lane_f64(best_s, win);
-    sum += w;
-    if (lane == j) {
-      my_id = id;
-      my_w = w;
-    }
-    if (lane == win) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i == best_i) key[i] = 0;
-      lane_best();
-    }
+    for (int j = 0; j < k; ++j) sum += read_lane_f64(w, j);
+    w = sum > 0.0 ? w / sum : 0.0;
   }
   if (lane < k) {
-    double w = my_w;
-    if (o.renorm) w = sum > 0.0 ? w / sum : 0.0;
-    ids[(int64_t)t * k + lane] = my_id;
+    ids[(int64_t)t * k + lane] = p.id;
     gates[(int64_t)t * k + lane] = (float)(w * (double)o.scale);
   }
 }

@@ -120,6 +120,27 @@ def test_route_keeps_scores_apart_that_fp32_would_merge():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group", [(60, 1, 1), (256, 8, 3), (384, 1, 1)])
+def test_route_choices_that_fp32_cannot_make(score, E, n_group, topk_group):
+    """A bias that takes nearly all of each score away: the choice values differ by parts in 10^8, and order as in
+    64 bits (whose own rounding is 10^8 times smaller).  Near logits without a bias, large and small ones likewise."""
+    g = gen(E)
+    l = normal(g, 50, E, std=1.0, dtype=torch.float32)
+    l[:] = l[0]                                  # one bias for all rows
+    l += (torch.rand(50, E, generator=g) - 0.5) * 2e-6
+    bias = -scores64(l[:1], score)[0][0].float()
+    near = normal(g, 50, 1, std=1.0, dtype=torch.float32) + torch.rand(50, E, generator=g) * 1e-6
+    far = torch.where(torch.rand(50, E, generator=g) < 0.5, 22.0, -640.0) + torch.rand(50, E, generator=g) * 15
+    for x, b in ((l, bias), (near, None), (far, None), (far, bias), (near, bias)):
+        for top in (1, 2):
+            a = (6, score, b, n_group, topk_group, top, True, 1.0)
+            ids, gates = qgg.moe_route_scored(x.to(DEV), 6, score, None if b is None else b.to(DEV), *a[3:])
+            rid, rg = route64(x, *a)
+            assert torch.equal(ids.cpu(), rid)
+            assert torch.all((gates.cpu().double() - rg).abs() <= 1.01 * H32 * rg.abs() + 1e-44)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_values_that_are_not_finite(score):
     g = gen(5)
     l = normal(g, 6, 96, dtype=torch.float32)
