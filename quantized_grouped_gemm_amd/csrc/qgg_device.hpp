@@ -98,6 +98,22 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Sum over the wavefront, in lane 63 (a fixed order).
+__device__ __forceinline__ float wave_sum_63(float v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(
+        0, __float_as_int(v), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});    // quad_perm 1,0,3,2
+  add(integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});    // quad_perm 2,3,0,1
+  add(integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});   // row_half_mirror
+  add(integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});   // row_mirror
+  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // row_bcast:15
+  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});   // row_bcast:31
+  return v;
+}
+
 // E8M0 exponent code -> fp32 scale 2^(c-127); code 0 is the subnormal 2^-127,
 // code 255 is NaN.
 __device__ __forceinline__ float e8m0_to_f32(uint32_t c) {

@@ -41,25 +41,6 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return v;
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-  for (int off = 32; off; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-  return v;
-}
-
-__device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
-}
-
-__device__ __forceinline__ double read_lane_f64(double v, int lane) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-}
-
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   auto step = [&](auto ctrl, auto rows) {
     v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value,
@@ -79,6 +60,22 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// maximum of values that are not NaN
+__device__ __forceinline__ float wave_max_f32(float v) {
+  return key_value(wave_max_u32(order_key(v)));
+}
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_63(v)), 63));
+}
+
+__device__ __forceinline__ double read_lane_f64(double v, int lane) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
 __device__ __forceinline__ float read_lane_f32(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
@@ -91,21 +88,12 @@ __device__ __forceinline__ int group_shift(int n_group) {
   return sh;
 }
 
-// A token's choice: lane j < k holds the id and the logit of its j-th expert.
-struct Pick {
-  int id;
-  float l;
-};
-
 // k rounds of a wavefront arg-max over the lanes' keys (0: no candidate); among
-// equal keys the lowest id.  MaxKey is the maximum over the wavefront, `each`
-// gets every round's key in order, and the next one's after the last round.
-template <int NV, typename K, typename MaxKey, typename Each>
-__device__ __forceinline__ Pick take(K (&key)[NV], const float (&l)[NV], int k, int lane,
-                                     MaxKey max_key, Each each) {
-  K best = 0;
-  int best_i = 0;
-  float best_l = 0.f;
+// equal keys the lowest id.  Lane j < k ends with the j-th id.
+template <int NV>
+__device__ __forceinline__ int take64(uint64_t (&key)[NV], int k, int lane) {
+  uint64_t best = 0;
+  int best_i = 0, my_id = 0;
   auto lane_best = [&]() {
     best = 0;
 #pragma unroll
@@ -113,14 +101,11 @@ __device__ __forceinline__ Pick take(K (&key)[NV], const float (&l)[NV], int k, 
       if (key[i] > best) {
         best = key[i];
         best_i = i;
-        best_l = l[i];
       }
   };
   lane_best();
-  Pick p{0, -INFINITY};
   for (int j = 0; j < k; ++j) {
-    const K top = max_key(best);
-    each(j, top);
+    const uint64_t top = wave_max_u64(best);
     uint64_t holders = __ballot(best == top);
     int win = __ffsll((unsigned long long)holders) - 1;
     int id = 64 * __builtin_amdgcn_readlane(best_i, win) + win;
@@ -132,11 +117,7 @@ __device__ __forceinline__ Pick take(K (&key)[NV], const float (&l)[NV], int k, 
         win = h;
       }
     }
-    const float wl = read_lane_f32(best_l, win);
-    if (lane == j) {
-      p.id = id;
-      p.l = wl;
-    }
+    if (lane == j) my_id = id;
     if (lane == win) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -144,8 +125,63 @@ __device__ __forceinline__ Pick take(K (&key)[NV], const float (&l)[NV], int k, 
       lane_best();
     }
   }
-  each(k, max_key(best));
-  return p;
+  return my_id;
+}
+
+// The same on 32-bit keys whose low four bits are 15 - i (entry i of a lane is
+// expert 64 i + lane): the key itself then says which entry it is, and equal
+// values go to the lower id by the order of keys and lanes alone.  *gap: the
+// least difference of neighbours in the order, the first one not taken
+// included; with TIES equal values count as no neighbours.
+constexpr uint32_t kEntry = 15;
+
+template <int NV, bool TIES>
+__device__ __forceinline__ int take32(uint32_t (&key)[NV], int k, int lane, float* first,
+                                      float* last, float* gap) {
+  int my_id = 0;
+  float prev = 0.f, least = INFINITY;
+  for (int j = 0;; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
+    const uint32_t top = wave_max_u32(best);
+    if (top == 0) break;                         // nothing left (j = k at the earliest)
+    const float v = key_value(top & ~kEntry);
+    if (j == 0) *first = v;
+    else if (!TIES || v != prev) least = fminf(least, prev - v);
+    prev = v;
+    if (j == k) break;
+    const int win = __ffsll((unsigned long long)__ballot(best == top)) - 1;
+    const int id = 64 * (int)(kEntry - (top & kEntry)) + win;
+    if (lane == j) my_id = id;
+    const uint32_t gone = lane == win ? top : 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = key[i] == gone ? 0u : key[i];
+  }
+  *last = prev;
+  *gap = least;
+  return my_id;
+}
+
+// The value of a lane of the other half of a block of 2 off lanes, all of whose
+// halves are uniform.
+__device__ __forceinline__ int partner_bits(int v, int off) {
+  switch (off) {
+    case 1: return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);    // quad_perm 1,0,3,2
+    case 2: return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);    // quad_perm 2,3,0,1
+    case 4: return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);   // row_half_mirror
+    case 8: return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);   // row_mirror
+    default: return __shfl_xor(v, off, kWave);
+  }
+}
+__device__ __forceinline__ float partner(float v, int off) {
+  return __int_as_float(partner_bits(__float_as_int(v), off));
+}
+__device__ __forceinline__ double partner(double v, int off) {
+  const long long u = __double_as_longlong(v);
+  const uint32_t lo = partner_bits((int)(u & 0xFFFFFFFF), off);
+  const uint32_t hi = partner_bits((int)(u >> 32), off);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
 // Two best of each group from the wavefront's row of choice values: the lane's
@@ -162,7 +198,7 @@ __device__ __forceinline__ void group_best(const F* row, int size, int n_group, 
       b1 = max(b1, v);
     }
   for (int off = 1; off < per; off <<= 1) {
-    const F o1 = __shfl_xor(b1, off, kWave), o2 = __shfl_xor(b2, off, kWave);
+    const F o1 = partner(b1, off), o2 = partner(b2, off);
     b2 = max(min(b1, o1), max(b2, o2));
     b1 = max(b1, o1);
   }
@@ -186,7 +222,7 @@ __device__ __forceinline__ uint64_t keep_groups(F score, const RouteOpts& o, int
 
 // The choice in double.
 template <int NV>
-__device__ __forceinline__ Pick choose64(const float (&l)[NV], const float* bias, int E, int k,
+__device__ __forceinline__ int choose64(const float (&l)[NV], const float* bias, int E, int k,
                                          const RouteOpts& o, int lane, double* row) {
   double c[NV];
   if (o.softmax) {
@@ -230,28 +266,29 @@ __device__ __forceinline__ Pick choose64(const float (&l)[NV], const float* bias
       if (e < E && !((kept >> ((e / size) << sh)) & 1)) key[i] = 0;
     }
   }
-  return take<NV>(key, l, k, lane, [](uint64_t v) { return wave_max_u64(v); },
-                  [](int, uint64_t) {});
+  return take64<NV>(key, k, lane);
 }
 
 // The choice in fp32; *sure is false where a comparison that decided lies
 // within its error.  Errors, in absolute terms: a sigmoid is off by (|l| + 6)
 // half steps of e / (1 + e)^2 or of itself, under 8 in all (2^-21); a softmax
 // by |l - max| + 24 half steps of p, under 25 (2^-19); the bias adds half a
-// step of the sum.
-template <int NV>
-__device__ __forceinline__ Pick choose32(const float (&l)[NV], const float* bias, int E, int k,
-                                         const RouteOpts& o, int lane, float* row, bool* sure) {
+// step of the sum, the cut of a key's low bits 2^-20 of what it holds.  EXACT:
+// the logits are BF16, which the cut leaves whole, so that equal keys are equal
+// logits.
+template <int NV, bool EXACT, typename LoadL>
+__device__ __forceinline__ int choose32(const float (&l)[NV], const float* bias, int E, int k,
+                                         const RouteOpts& o, int lane, float* row, LoadL load_l, bool* sure) {
   const bool grouped = o.topk_group < o.n_group;
   const bool by_score = bias || (grouped && o.group_top == 2);
   const float err = o.softmax ? 0x1p-19f : 0x1p-21f;
   float x[NV], c[NV];                            // what orders experts; what orders groups
   float m = -INFINITY;
-  if (o.softmax) {
-    uint32_t mk = 0;
+  if (o.softmax && by_score) {
+    m = l[0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) mk = max(mk, order_key(l[i]));
-    m = key_value(wave_max_u32(mk));
+    for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
+    m = wave_max_f32(m);
   }
   if (by_score) {
     if (o.softmax) {
@@ -281,19 +318,11 @@ __device__ __forceinline__ Pick choose32(const float (&l)[NV], const float* bias
     x[i] = bias ? c[i] : l[i];
     if (!by_score) c[i] = l[i];
   }
-  // Logits order as their scores do in double unless they are so near that the
-  // scores round to one number, or so large or small that the scores do.
-  auto near = [&](float hi, float lo) {          // hi >= lo, both compared as x
-    if (hi == lo) return bias != nullptr && hi != -INFINITY;
-    if (bias) return !(hi - lo > 2.0f * err + 0x1p-22f * fmaxf(fabsf(hi), fabsf(lo)));
-    const float top = o.softmax ? hi - m : hi, low = o.softmax ? lo - m : lo;
-    return !(hi - lo > 1e-9f) || top > 20.0f || (low < -600.0f && lo != -INFINITY);
-  };
   bool ok = true;
   uint32_t key[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    key[i] = lane + 64 * i < E ? order_key(x[i] + 0.0f) : 0;   // -0 -> +0
+  for (int i = 0; i < NV; ++i)                   // -0 -> +0; above 0 even for -inf
+    key[i] = lane + 64 * i < E ? (order_key(x[i] + 0.0f) & ~kEntry) | (kEntry - i) : 0;
   if (grouped) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -312,25 +341,32 @@ __device__ __forceinline__ Pick choose32(const float (&l)[NV], const float* bias
     }
     if (by_score) ok = lo == hi ? lo == -INFINITY
                                 : lo - hi > 4.0f * err + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi));
-    else ok = !near(lo, hi);
+    else ok = lo == hi || lo - hi > 1e-9f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 64 * i;
       if (e < E && !((kept >> ((e / size) << sh)) & 1)) key[i] = 0;
     }
   }
-  float prev = 0.f;
-  const Pick p = take<NV>(key, l, k, lane, [](uint32_t v) { return wave_max_u32(v); },
-                          [&](int j, uint32_t top) {
-                            const float v = key_value(top);
-                            if (j > 0 && top != 0 && near(prev, v)) ok = false;
-                            prev = v;
-                          });
-  // softmax gates are formed from the kept logits alone; where the whole row's
-  // sum would round their scores to zero, the other path says so
-  if (o.softmax && bias && __any(lane < k && p.l - m < -600.0f && p.l != -INFINITY)) ok = false;
+  float first = 0.f, last = 0.f, gap;
+  int id;
+  if (EXACT && !bias) id = take32<NV, true>(key, k, lane, &first, &last, &gap);
+  else id = take32<NV, false>(key, k, lane, &first, &last, &gap);
+  const float size = fmaxf(fabsf(first), fabsf(last));
+  if (bias) {
+    ok &= gap > 2.0f * err + 0x1p-18f * size;
+    // softmax gates are formed from the kept logits alone; where the whole
+    // row's sum would round their scores to zero, the other path says so
+    const float kl = lane < k ? load_l(id) : m;
+    if (o.softmax && __any(kl - m < -600.0f)) ok = false;
+  } else {
+    // logits order as their scores do in double, unless they are so near, or
+    // so large or small, that scores round to one number
+    ok &= gap > (EXACT ? 1e-9f : 1e-9f + 0x1p-18f * size);
+    ok &= o.softmax ? last - (by_score ? m : first) > -600.0f : first < 20.0f && last > -600.0f;
+  }
   *sure = ok;
-  return p;
+  return id;
 }
 
 // One wavefront per token; lane l holds experts l, l + 64, ... (NV of them).
@@ -363,36 +399,43 @@ __global__ __launch_bounds__(256) void k_route_scored(const L* __restrict__ logi
   }
   if (err && __any(bad) && lane == 0) atomicOr(err, 1);
 
+  auto load_l = [&](int e) {
+    const float x = load_logit(row + e);
+    return __builtin_isfinite(x) ? x : -INFINITY;
+  };
   bool sure;
-  Pick p = choose32<NV>(l, bias, E, k, o, lane, reinterpret_cast<float*>(mine), &sure);
-  double m = -INFINITY, total = 0.0;             // softmax: maximum and sum of the row
+  int id = choose32<NV, sizeof(L) == 2>(l, bias, E, k, o, lane, reinterpret_cast<float*>(mine),
+                                        load_l, &sure);
   if (!sure) {
     wave_lds_sync();
-    p = choose64<NV>(l, bias, E, k, o, lane, mine);
+    id = choose64<NV>(l, bias, E, k, o, lane, mine);
   }
+  const float kl = lane < k ? load_l(id) : -INFINITY;
+  double m = 0.0, total = 1.0;                   // softmax: maximum and sum of the row
   if (o.softmax) {
-    uint32_t mk = 0;
+    if (o.renorm && sure) {                      // any common factor cancels
+      m = (double)wave_max_f32(kl);
+    } else {
+      float top = l[0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) mk = max(mk, order_key(l[i]));
-    m = (double)key_value(wave_max_u32(mk));
-    if (!o.renorm || !sure) {
+      for (int i = 1; i < NV; ++i) top = fmaxf(top, l[i]);
+      m = (double)wave_max_f32(top);
+      total = 0.0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) total += l[i] == -INFINITY ? 0.0 : exp((double)l[i] - m);
       total = wave_sum_f64(total);
     }
   }
   double w = 0.0;
-  if (lane < k && p.l != -INFINITY) {
-    w = o.softmax ? exp((double)p.l - m) : 1.0 / (1.0 + exp(-(double)p.l));
-    if (o.softmax && (!o.renorm || !sure)) w /= total;
-  }
+  if (kl != -INFINITY)
+    w = o.softmax ? exp((double)kl - m) / total : 1.0 / (1.0 + exp(-(double)kl));
   if (o.renorm) {
     double sum = 0.0;
     for (int j = 0; j < k; ++j) sum += read_lane_f64(w, j);
     w = sum > 0.0 ? w / sum : 0.0;
   }
   if (lane < k) {
-    ids[(int64_t)t * k + lane] = p.id;
+    ids[(int64_t)t * k + lane] = id;
     gates[(int64_t)t * k + lane] = (float)(w * (double)o.scale);
   }
 }
