@@ -872,9 +872,9 @@ qgg_status moe_ffn_bwd_lora(const qgg_qweight* w_gate_up, const qgg_qweight* w_d
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-static RouteOpts route_opts(const qgg_route_opts* o) {
+static RouteOpts route_opts(const qgg_route_opts* o, int size) {
   return RouteOpts{o->score == QGG_SCORE_SOFTMAX, o->n_group, o->topk_group, o->group_top,
-                   o->renorm != 0, o->scale};
+                   o->renorm != 0, o->scale, (uint32_t)(((1 << 20) + size - 1) / size)};
 }
 
 static bool valid_score(const qgg_route_opts* o, int logits_type) {
@@ -893,7 +893,8 @@ qgg_status moe_route_scored(const void* logits, int logits_type, const float* bi
     return QGG_ERR_INVALID_ARG;
   if (opts->topk_group < G && G > 64) return QGG_ERR_UNSUPPORTED;
   if (T > 0 && (!logits || !topk_ids || !topk_gates)) return QGG_ERR_INVALID_ARG;
-  QGG_HIP(launch_route_scored(logits, logits_type == QGG_BF16, bias, T, E, k, route_opts(opts),
+  QGG_HIP(launch_route_scored(logits, logits_type == QGG_BF16, bias, T, E, k,
+                              route_opts(opts, E / G),
                               topk_ids, topk_gates, err_flag, stream));
   return QGG_OK;
 }
@@ -904,7 +905,7 @@ qgg_status moe_route_scored_bwd(const void* logits, int logits_type, const int32
   if (!valid_route_dims(T, E, k) || !valid_score(opts, logits_type)) return QGG_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_ids || !dgates || !dlogits)) return QGG_ERR_INVALID_ARG;
   QGG_HIP(launch_route_scored_bwd(logits, logits_type == QGG_BF16, topk_ids, dgates, T, E, k,
-                                  route_opts(opts), dlogits, stream));
+                                  route_opts(opts, E), dlogits, stream));
   return QGG_OK;
 }
 

@@ -155,6 +155,9 @@ struct RouteOpts {
   int n_group, topk_group, group_top;
   bool renorm;
   float scale;
+  uint32_t magic;                // ceil(2^20 / experts of a group)
+  // expert e < 1024 is of group floor(e / size): e (magic size - 2^20) < 2^20
+  __host__ __device__ int group_of(int e) const { return (int)(((uint32_t)e * magic) >> 20); }
 };
 hipError_t launch_route_scored(const void* logits, bool bf16, const float* bias, int T, int E,
                                int k, const RouteOpts& o, int32_t* ids, float* gates, int32_t* err,

@@ -130,37 +130,48 @@ __device__ __forceinline__ int take64(uint64_t (&key)[NV], int k, int lane) {
 
 // The same on 32-bit keys whose low four bits are 15 - i (entry i of a lane is
 // expert 64 i + lane): the key itself then says which entry it is, and equal
-// values go to the lower id by the order of keys and lanes alone.  *gap: the
-// least difference of neighbours in the order, the first one not taken
-// included; with TIES equal values count as no neighbours.
+// values go to the lower id by the order of keys and lanes alone.  Each lane
+// sorts its keys once, so that a round looks at one key a lane and the lane that
+// gives one moves up the rest.  Lane j <= k ends with the j-th key in *order
+// (the k-th one not taken; 0: none left).
 constexpr uint32_t kEntry = 15;
 
-template <int NV, bool TIES>
-__device__ __forceinline__ int take32(uint32_t (&key)[NV], int k, int lane, float* first,
-                                      float* last, float* gap) {
-  int my_id = 0;
-  float prev = 0.f, least = INFINITY;
+template <int NV>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[NV]) {
+#pragma unroll
+  for (int size = 2; size <= NV; size *= 2)      // bitonic
+#pragma unroll
+    for (int step = size / 2; step; step /= 2)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = i ^ step;
+        if (j > i) {
+          const uint32_t hi = max(v[i], v[j]), lo = min(v[i], v[j]);
+          const bool down = (i & size) == 0;
+          v[i] = down ? hi : lo;
+          v[j] = down ? lo : hi;
+        }
+      }
+}
+
+template <int NV>
+__device__ __forceinline__ int take32(uint32_t (&key)[NV], int k, int lane, uint32_t* order) {
+  sort_down<NV>(key);
+  uint32_t keys = 0;
+  int ids = 0;
   for (int j = 0;; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-    const uint32_t top = wave_max_u32(best);
-    if (top == 0) break;                         // nothing left (j = k at the earliest)
-    const float v = key_value(top & ~kEntry);
-    if (j == 0) *first = v;
-    else if (!TIES || v != prev) least = fminf(least, prev - v);
-    prev = v;
+    const uint32_t top = wave_max_u32(key[0]);
+    keys = lane == j ? top : keys;
     if (j == k) break;
-    const int win = __ffsll((unsigned long long)__ballot(best == top)) - 1;
-    const int id = 64 * (int)(kEntry - (top & kEntry)) + win;
-    if (lane == j) my_id = id;
-    const uint32_t gone = lane == win ? top : 0u;
+    const int win = __ffsll((unsigned long long)__ballot(key[0] == top)) - 1;
+    ids = lane == j ? 64 * (int)(kEntry - (top & kEntry)) + win : ids;
+    const bool mine = lane == win;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = key[i] == gone ? 0u : key[i];
+    for (int i = 0; i + 1 < NV; ++i) key[i] = mine ? key[i + 1] : key[i];
+    key[NV - 1] = mine ? 0u : key[NV - 1];
   }
-  *last = prev;
-  *gap = least;
-  return my_id;
+  *order = keys;
+  return ids;
 }
 
 // The value of a lane of the other half of a block of 2 off lanes, all of whose
@@ -263,7 +274,7 @@ __device__ __forceinline__ int choose64(const float (&l)[NV], const float* bias,
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 64 * i;
-      if (e < E && !((kept >> ((e / size) << sh)) & 1)) key[i] = 0;
+      if (e < E && !((kept >> (o.group_of(e) << sh)) & 1)) key[i] = 0;
     }
   }
   return take64<NV>(key, k, lane);
@@ -345,26 +356,31 @@ __device__ __forceinline__ int choose32(const float (&l)[NV], const float* bias,
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 64 * i;
-      if (e < E && !((kept >> ((e / size) << sh)) & 1)) key[i] = 0;
+      if (e < E && !((kept >> (o.group_of(e) << sh)) & 1)) key[i] = 0;
     }
   }
-  float first = 0.f, last = 0.f, gap;
-  int id;
-  if (EXACT && !bias) id = take32<NV, true>(key, k, lane, &first, &last, &gap);
-  else id = take32<NV, false>(key, k, lane, &first, &last, &gap);
-  const float size = fmaxf(fabsf(first), fabsf(last));
+  uint32_t order;
+  const int id = take32<NV>(key, k, lane, &order);
+  // lane j in 1 .. k compares the j-th value with the one before it
+  const float v = key_value(order & ~kEntry);
+  const float prev = __shfl_up(v, 1, kWave);
+  const bool next = lane >= 1 && lane <= k && order != 0;
+  bool close;
   if (bias) {
-    ok &= gap > 2.0f * err + 0x1p-18f * size;
+    close = !(prev - v > 2.0f * err + 0x1p-18f * fmaxf(fabsf(prev), fabsf(v)));
     // softmax gates are formed from the kept logits alone; where the whole
     // row's sum would round their scores to zero, the other path says so
-    const float kl = lane < k ? load_l(id) : m;
-    if (o.softmax && __any(kl - m < -600.0f)) ok = false;
+    if (o.softmax && lane < k && !(load_l(id) - m > -600.0f)) ok = false;
   } else {
     // logits order as their scores do in double, unless they are so near, or
     // so large or small, that scores round to one number
-    ok &= gap > (EXACT ? 1e-9f : 1e-9f + 0x1p-18f * size);
-    ok &= o.softmax ? last - (by_score ? m : first) > -600.0f : first < 20.0f && last > -600.0f;
+    const float top = o.softmax ? (by_score ? m : read_lane_f32(v, 0)) : 0.f;
+    close = EXACT ? prev != v && !(prev - v > 1e-9f)
+                  : !(prev - v > 1e-9f + 0x1p-18f * fmaxf(fabsf(prev), fabsf(v)));
+    close |= !(v - top > -600.0f) || (!o.softmax && prev > 20.0f);
   }
+  ok &= !(next && close);
+  ok = __all(ok);
   *sure = ok;
   return id;
 }
