@@ -176,9 +176,10 @@ struct RowCopy {
   // taken to be empty
   __device__ __forceinline__ void copy_whole(int st, int steps, int wave, uint8_t* buf) const {
     const __amdgpu_buffer_rsrc_t rsrc = raw_buffer(a, st < steps ? bytes : 0u);
+    const uint32_t at = st < steps ? (uint32_t)st * 128u : 0u;
 #pragma unroll
     for (int i = 0; i < NCA; ++i)
-      copy16_to_lds(rsrc, off[i], (uint32_t)st * 128u, buf + (256 * i + 64 * wave) * 16);
+      copy16_to_lds(rsrc, off[i], at, buf + (256 * i + 64 * wave) * 16);
   }
   // step `st` of any width
   __device__ __forceinline__ void copy_part(int st, int red, int wave, uint8_t* buf) const {
@@ -234,13 +235,9 @@ __device__ __forceinline__ void stage_w_scales(const void* scales, int64_t at, i
 
 // MB scale bytes of a lane as MFMA scale operand: block mb is byte mb.
 template <int MB>
-__device__ __forceinline__ void read_scales(const uint8_t* sc, int st, int i16, int x[2]) {
+__device__ __forceinline__ int read_scales(const uint8_t* sc, int st, int i16) {
   const uint8_t* at = sc + (st * 16 + i16) * MB;
-  if constexpr (MB == 4) {
-    x[0] = *reinterpret_cast<const int*>(at);
-  } else {
-    x[0] = *reinterpret_cast<const uint16_t*>(at);
-  }
+  return MB == 4 ? *reinterpret_cast<const int*>(at) : *reinterpret_cast<const uint16_t*>(at);
 }
 
 // Rows of block mb; `at` = offset of the first of the lane's two chunks
@@ -274,7 +271,7 @@ __device__ __forceinline__ void mfma_block(const i32x8_t& w, const i32x8_t& x, u
 // reads, four MFMAs, two reads, ...).
 template <bool WF32, int NMB>
 __device__ __forceinline__ void mfma_step(const uint8_t* as, const WStep& w, uint32_t ws,
-                                          const int xs[2], int at, f32x4_t (&acc)[NMB][4]) {
+                                          int xs, int at, f32x4_t (&acc)[NMB][4]) {
   using std::integral_constant;
   i32x8_t x = read_rows(as, 0, at);
   auto row_block = [&](auto mbc) {
@@ -284,7 +281,7 @@ __device__ __forceinline__ void mfma_step(const uint8_t* as, const WStep& w, uin
       if constexpr (mb + 1 < NMB) nx = read_rows(as, mb + 1, at);
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb)
-        mfma_block<WF32, (mb & 3)>(w.w[nb], x, ws, xs[mb >> 2], acc[mb][nb]);
+        mfma_block<WF32, mb>(w.w[nb], x, ws, xs, acc[mb][nb]);
       x = nx;
     }
   };
@@ -292,10 +289,6 @@ __device__ __forceinline__ void mfma_step(const uint8_t* as, const WStep& w, uin
   row_block(integral_constant<int, 1>{});
   row_block(integral_constant<int, 2>{});
   row_block(integral_constant<int, 3>{});
-  row_block(integral_constant<int, 4>{});
-  row_block(integral_constant<int, 5>{});
-  row_block(integral_constant<int, 6>{});
-  row_block(integral_constant<int, 7>{});
 }
 
 template <bool WF32, int NMB>
@@ -374,8 +367,7 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
     // the other object
     auto kstage = [&](int i, WRaw& raw, const uint8_t* rows, uint8_t* next) {
       rc.copy_whole(st0 + i + kNBuf - 1, steps, wave, next);
-      int xs[2];
-      read_scales<MB>(sc, i, i16, xs);
+      const int xs = read_scales<MB>(sc, i, i16);
       const uint32_t ws = wt[wave * kPiece + i];
       WStep w;
 #pragma unroll
@@ -478,8 +470,7 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
         w.w[nb][2 * t] = v[0];
         w.w[nb][2 * t + 1] = v[1];
       }
-    int xs[2];
-    read_scales<MB>(sc, st % kPiece, i16, xs);
+    const int xs = read_scales<MB>(sc, st % kPiece, i16);
     mfma_step<WF32, NMB>(as, w, wt[wave * kPiece + st % kPiece], xs, at, acc);
     __syncthreads();
   }
@@ -548,6 +539,7 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm(Fp8GemmArgs g, int ntn) {
 // (64 columns each).  Rows and weights both pass through LDS, two stages of 64
 // KiB: every byte that a workgroup asks its L2 for is used by 256 rows or
 // columns, which is what bounds a product of this size (see launch_sized).
+constexpr int kBigBlocks = 18;
 struct BigStage {
   uint8_t* a;                                    // [256][128]
   uint8_t* w;                                    // y = a W^T: [256 columns][128]
@@ -568,9 +560,9 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
   // row copies: slot tid & 7 of rows 64 i + tid / 8
   const uint32_t abytes = (uint32_t)(g.a_rows * red);
   const int acol = ((tid & 7) ^ swz_a(tid >> 3)) * 16;
-  uint32_t aoff[4];
+  uint32_t aoff[NMB > 8 ? 5 : 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < (NMB > 8 ? 5 : 4); ++i) {
     const int r = 64 * i + (tid >> 3);
     const int rr = it.row0 + (r < it.nrows ? r : 0);
     const uint32_t src = g.tokens ? g.perm[rr] / g.topk : rr;
@@ -579,41 +571,41 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
   // weight copies
   const uint32_t wbytes = (uint32_t)g.N * (uint32_t)g.K;
   const uint8_t* wbase = g.w + (int64_t)it.expert * wbytes;
-  uint32_t woff[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (TRANS) {
-      // wavefront: 32 rows of one column group; slot 4 r + s holds chunk s ^ swz_t(r)
-      const int grp = wave >> 1;
-      const int r = (wave & 1) * 64 + 16 * i + (lane >> 2);
-      const int chunk = (lane & 3) ^ swz_t(r);
-      const int c = min(it.nt * 256 + 64 * grp, cols - 64);
-      woff[i] = (uint32_t)r * (uint32_t)g.K + (uint32_t)(c + 16 * chunk);
-    } else {
-      const int c = min(it.nt * 256 + 64 * i, cols - 64) + (tid >> 3);
-      woff[i] = (uint32_t)c * (uint32_t)g.K + (uint32_t)(((tid & 7) ^ swz_w(tid >> 3)) * 16);
-    }
+  uint32_t woff;
+  if constexpr (TRANS) {
+    // wavefront: 64 rows of one column group; slot 4 r + s holds chunk s ^ swz_t(r)
+    const int r = (wave & 1) * 64 + (lane >> 2);
+    const int c = min(it.nt * 256 + 64 * (wave >> 1), cols - 64);
+    woff = (uint32_t)r * (uint32_t)g.K + (uint32_t)(c + 16 * ((lane & 3) ^ swz_t(r)));
+  } else {
+    woff = (uint32_t)(tid >> 3) * (uint32_t)g.K + (uint32_t)(((tid & 7) ^ swz_w(tid >> 3)) * 16);
   }
   // (copies that are not wanted, of rows past the tile or steps past the piece,
   // read an empty buffer: no branches, and every step issues the same number)
   auto copy_a = [&](int st, bool live, const BigStage& s) {
     const bool in = TRANS ? st * 128 + acol < red : true;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      copy16_to_lds(raw_buffer(g.a, live && 4 * i < blocks ? abytes : 0u),
-                    in ? aoff[i] : 0xFFFFFFF0u - (uint32_t)st * 128u, (uint32_t)st * 128u,
+    const uint32_t at = live ? (uint32_t)st * 128u : 0u;
+    auto copy = [&](int i, bool wanted) {
+      copy16_to_lds(raw_buffer(g.a, wanted ? abytes : 0u), in ? aoff[i] : 0xFFFFFFF0u - at, at,
                     s.a + (512 * i + 64 * wave) * 16);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy(i, live && 4 * i < blocks);
+    if (NMB > 8 && wave < 4) copy(4, live);      // rows 256 .. 287
   };
   auto copy_w = [&](int st, bool live, const BigStage& s) {
     const __amdgpu_buffer_rsrc_t rsrc = raw_buffer(wbase, live ? wbytes : 0u);
+    const uint32_t s0 = live ? st : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (TRANS) {
         // W rows past N lie past the buffer's end
-        copy16_to_lds(rsrc, woff[i] + (uint32_t)st * 128u * (uint32_t)g.K, 0,
+        copy16_to_lds(rsrc, woff + (s0 * 128u + 16u * i) * (uint32_t)g.K, 0,
                       s.w + (wave >> 1) * 8192 + (wave & 1) * 4096 + i * 1024);
       } else {
-        copy16_to_lds(rsrc, woff[i], (uint32_t)st * 128u, s.w + (512 * i + 64 * wave) * 16);
+        const uint32_t c = min(it.nt * 256 + 64 * i, cols - 64);
+        copy16_to_lds(rsrc, woff, c * (uint32_t)g.K + s0 * 128u,
+                      s.w + (512 * i + 64 * wave) * 16);
       }
     }
   };
@@ -635,63 +627,99 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
 #pragma unroll
     for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  auto read_w = [&](const BigStage& s, WStep& w) {
+  auto read_w = [&](const BigStage& s, int nb, WStep& w) {
     if constexpr (TRANS) {
       // reduced values 64 (q & 1) + 32 (q / 2) + 8 t .. + 7, columns 16 nb ..:
       // row r = tr_row + 8 t, chunk nb, whose slot is nb ^ swz_t(r)
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const i32x2_t v = lds_tr8(s.w + ((tr_at ^ (nb << 4)) + t * 512));
-          w.w[nb][2 * t] = v[0];
-          w.w[nb][2 * t + 1] = v[1];
-        }
+      for (int t = 0; t < 4; ++t) {
+        const i32x2_t v = lds_tr8(s.w + ((tr_at ^ (nb << 4)) + t * 512));
+        w.w[nb][2 * t] = v[0];
+        w.w[nb][2 * t + 1] = v[1];
+      }
     } else {
       // MFMA row i of block nb is column 16 (i / 4) + 4 nb + (i & 3)
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const int r = nq * 64 + 16 * (i16 >> 2) + 4 * nb + (i16 & 3);
-        const int o = r * 128 + (((4 * (q & 1) + 2 * (q >> 1)) ^ swz_w(r)) << 4);
-        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(s.w + o);
-        const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(s.w + (o ^ 16));
-        w.w[nb] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                          (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-      }
+      const int r = nq * 64 + 16 * (i16 >> 2) + 4 * nb + (i16 & 3);
+      const int o = r * 128 + (((4 * (q & 1) + 2 * (q >> 1)) ^ swz_w(r)) << 4);
+      const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(s.w + o);
+      const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(s.w + (o ^ 16));
+      w.w[nb] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                        (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
     }
   };
-  // Step i of n from stage s, rows of step i + 1 to stage t.  Once every
-  // wavefront holds its weights in registers their stage is free, so the
-  // weights of step i + 2 (which come from memory) start two steps ahead of
-  // their use, the rows (which the L2 mostly holds) one.
+  // Step i of n: its weights are in registers and its rows in s; rows of step
+  // i + 1 go to t.  The last two row blocks run column block by column block,
+  // and the registers of each one's weights are loaded for the next step behind
+  // its last use: the matrix core works on while LDS delivers them.  So the
+  // weights of step i + 2 (which come from memory) can start with step i, the
+  // rows of step i + 1 (which the L2 mostly holds) too.
+  WStep w;
   auto step = [&](int st0, int i, int n, const BigStage& s, const BigStage& t) {
     copy_a(st0 + i + 1, i + 1 < n, t);
-    WStep w;
-    read_w(s, w);
-    stage_barrier<63>();
     copy_w(st0 + i + 2, i + 2 < n, s);
-    int xs[2];
+    int xs[3];
     const uint2 v = *reinterpret_cast<const uint2*>(sc + ((i * 2 + half) * 16 + i16) * 8);
     xs[0] = (int)v.x;
     xs[1] = (int)v.y;
-    mfma_step<WF32, NMB>(s.a, w, wt[nq * kPiece + i], xs, ah, acc);
-    stage_barrier<4>();
+    xs[2] = NMB > 8 ? sc[kPiece * 256 + (i * 2 + half) * 16 + i16] : 0;
+    const uint32_t ws = wt[nq * kPiece + i];
+    i32x8_t x = read_rows(s.a, 0, ah);
+    auto row_block = [&](auto mbc) {
+      constexpr int mb = decltype(mbc)::value;
+      if constexpr (mb + 2 < NMB) {
+        const i32x8_t nx = read_rows(s.a, mb + 1, ah);
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+          mfma_block<WF32, (mb & 3)>(w.w[nb], x, ws, xs[mb >> 2], acc[mb][nb]);
+        x = nx;
+      }
+    };
+    using std::integral_constant;
+    row_block(integral_constant<int, 0>{});
+    row_block(integral_constant<int, 1>{});
+    row_block(integral_constant<int, 2>{});
+    row_block(integral_constant<int, 3>{});
+    row_block(integral_constant<int, 4>{});
+    row_block(integral_constant<int, 5>{});
+    row_block(integral_constant<int, 6>{});
+    const i32x8_t y = read_rows(s.a, NMB - 1, ah);
+    stage_barrier<8>();                          // weights of step i + 1 have landed
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      mfma_block<WF32, ((NMB - 2) & 3)>(w.w[nb], x, ws, xs[(NMB - 2) >> 2], acc[NMB - 2][nb]);
+      mfma_block<WF32, ((NMB - 1) & 3)>(w.w[nb], y, ws, xs[(NMB - 1) >> 2], acc[NMB - 1][nb]);
+      read_w(t, nb, w);
+    }
+    stage_barrier<4>();                          // and its rows
   };
 
+  const bool words = (steps & 3) == 0 && (reinterpret_cast<uintptr_t>(g.a_scales) & 3) == 0;
   for (int st0 = 0; st0 < steps; st0 += kPiece) {
     const int n = min(kPiece, steps - st0);
     copy_a(st0, true, s0);
     copy_w(st0, true, s0);
     copy_w(st0 + 1, n > 1, s1);
-    // scales: sc[step][half][row & 15][block of the half], wt[column group][step]
+    // scales: sc[step][half][row & 15][block of the half], those of a ninth block
+    // behind them, wt[column group][step]
     for (int v = tid; v < 32 * blocks; v += 512) {
       const int r = v >> 1, b = r >> 4, hb = b >= h0;
       const int rr = it.row0 + (r < it.nrows ? r : 0);
       const int64_t src = g.tokens ? g.perm[rr] / g.topk : rr;
       const uint8_t* row = g.a_scales + src * steps + st0;
-      uint8_t* out = sc + (hb * 16 + (r & 15)) * 8 + (b - hb * h0);
+      const int k = b - hb * h0, at = hb * 16 + (r & 15);
+      uint8_t* out = sc + (k < 8 ? at * 8 + k : kPiece * 256 + at);
+      const int stride = k < 8 ? 256 : 32;
+      if (words) {                               // n is a multiple of 4 then
 #pragma unroll 8
-      for (int j = v & 1; j < n; j += 2) out[j * 256] = row[j];
+        for (int w = v & 1; w < n / 4; w += 2) {
+          const uint32_t x = reinterpret_cast<const uint32_t*>(row)[w];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) out[(4 * w + j) * stride] = (uint8_t)(x >> (8 * j));
+        }
+      } else {
+#pragma unroll 8
+        for (int j = v & 1; j < n; j += 2) out[j * stride] = row[j];
+      }
     }
     if (half == 0)
       for (int j = lane; j < n; j += 64) {
@@ -700,6 +728,9 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
                                    : static_cast<const uint8_t*>(g.w_scales)[si];
       }
     stage_barrier<0>();
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) read_w(s0, nb, w);
+    stage_barrier<63>();
 #pragma nounroll
     for (int i = 0; i < n; i += 2) {
       step(st0, i, n, s0, s1);
@@ -736,17 +767,17 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
 
 template <bool TRANS, bool WF32>
 __global__ __launch_bounds__(512, 1) void k_fp8_gemm_big(Fp8GemmArgs g, int ntn) {
-  __shared__ __attribute__((aligned(16))) uint8_t a0[32768];
-  __shared__ __attribute__((aligned(16))) uint8_t a1[32768];
+  __shared__ __attribute__((aligned(16))) uint8_t a0[36864];
+  __shared__ __attribute__((aligned(16))) uint8_t a1[36864];
   __shared__ __attribute__((aligned(16))) uint8_t w0[32768];
   __shared__ __attribute__((aligned(16))) uint8_t w1[32768];
-  __shared__ __attribute__((aligned(16))) uint8_t sc[kPiece * 256];
+  __shared__ __attribute__((aligned(16))) uint8_t sc[kPiece * 288];
   __shared__ uint32_t wt[4 * kPiece];
   __shared__ int tiles_before[1025];
   __shared__ int scratch[16];
   __shared__ int item[4];
   const BigStage s0{a0, w0}, s1{a1, w1};
-  count_tiles(g.counts, g.E, 256, tiles_before, scratch);
+  count_tiles(g.counts, g.E, 16 * kBigBlocks, tiles_before, scratch);
   const int items = tiles_before[g.E] * ntn;
   const int per = (items + 7) >> 3;
   const int first = (blockIdx.x & 7) * per, last = min(first + per, items);
@@ -764,7 +795,8 @@ __global__ __launch_bounds__(512, 1) void k_fp8_gemm_big(Fp8GemmArgs g, int ntn)
       big_item<TRANS, WF32, decltype(n)::value>(g, it, s0, s1, sc, wt);
     };
     using std::integral_constant;
-    if (h0 > 6) run(integral_constant<int, 8>{});
+    if (h0 > 8) run(integral_constant<int, 9>{});
+    else if (h0 > 6) run(integral_constant<int, 8>{});
     else if (h0 > 5) run(integral_constant<int, 6>{});
     else if (h0 > 4) run(integral_constant<int, 5>{});
     else if (h0 > 2) run(integral_constant<int, 4>{});
@@ -785,7 +817,7 @@ int tile_blocks(const Fp8GemmArgs& g) {
 template <bool TRANS, bool WF32>
 static void launch_sized(const Fp8GemmArgs& g, hipStream_t s) {
   const int mb = tile_blocks(g);
-  const int mt = mb == 8 ? 256 : 16 * mb;
+  const int mt = 16 * (mb == 8 ? kBigBlocks : mb);
   const int64_t tiles = std::min<int64_t>(g.P, g.P / mt + g.E);
   const int ntn = ((TRANS ? g.K : g.N) + 255) / 256;
   // a multiple of 8: one stretch of items per XCD

@@ -626,6 +626,20 @@ def test_fp8_grouped_gemm(c, trans, f32):
         assert torch.equal(again, y)
 
 
+# one expert whose rows fill a tile of 288 to each of its heights, and the first that need two tiles; more than 64
+# blocks of reduced columns, so that the scales are staged twice
+@pytest.mark.parametrize("rows", [65, 97, 150, 190, 256, 257, 288, 289, 577])
+@pytest.mark.parametrize("trans", [False, True], ids=["nt", "t"])
+def test_fp8_grouped_gemm_tile_heights(rows, trans):
+    g = gen(rows)
+    N, K = (8384, 128) if trans else (128, 8448)
+    w = weights(g, 1, N, K, rows % 2 == 0)
+    p = perm_of(torch.zeros((rows, 1), dtype=torch.int32), 1)
+    x = qgg.fp8_quantize(normal(g, rows, N if trans else K).to(DEV))
+    flags = qgg.A_TOKENS | (qgg.TRANSPOSE_W if trans else 0)
+    check_gemm(w, x, p, rows, 1, flags, qgg.fp8_grouped_gemm(w, *x, p, rows, 1, flags=flags))
+
+
 def test_fp8_grouped_gemm_one_hot_reads_every_weight():
     # rows that are unit vectors read W back exactly, in both directions
     g = gen(77)
@@ -744,7 +758,7 @@ def test_layer_together():
         o = torch.bmm(W2[ids[:, j]], (torch.nn.functional.silu(h[:, :I]) * h[:, I:])[:, :, None])[:, :, 0]
         y = y + gates[:, j:j + 1] * o
     (y * dy.cpu().double()).sum().backward()
-    far = lambda u, v: float((u.cpu().double() - v).norm() / v.norm())  # noqa: E731
+    far = lambda u, v: float((u.detach().cpu().double() - v.detach()).norm() / v.detach().norm())  # noqa: E731
     # a rounding to E4M3 is uniform within half a step: 2^-4 / sqrt 3 = 3.6 % of a value at most, rms.  y passes two
     # (x, a), the second on values that carry the first through a product of two factors (x sqrt 2); dx four (dy, h twice
     # through u and silu', dh); dgates the same with dy and h.  Root of the sums of squares, and a margin of 1.5:
