@@ -34,8 +34,8 @@ typedef int i32x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ int swz_a(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
 // columns 64 g + 16 (i / 4) + 4 nb + i % 4 of W, i = 0 .. 15, 128 bytes each
 __device__ __forceinline__ int swz_w(int r) { return ((r >> 1) & 1) | ((r >> 3) & 6); }
-// rows of W r0 + 0 .. 7 and r0 + 64 .. 71, 64 bytes each
-__device__ __forceinline__ int swz_t(int r) { return ((r >> 1) & 2) | ((r >> 6) & 1); }
+// rows of W r0 + 0 .. 7 and r0 + 64 .. 71, 256 bytes each
+__device__ __forceinline__ int swz_t(int r) { return (r & 7) | ((r >> 3) & 8); }
 
 // Eight rows x 16 columns of bytes by a transposing LDS read: within each
 // 16-lane group, lane p points at eight bytes (row p / 2, half p & 1) and
@@ -341,7 +341,8 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
 #pragma unroll
       for (int j = 0; j < 4; ++j)                // row 16 a + 4 nb + j
         w.r[pr][j] = __builtin_amdgcn_raw_buffer_load_b128(
-            wrsrc, wv, (uint32_t)s * 128u + (uint32_t)(8 * pr + j) * (uint32_t)g.K, 0);
+            wrsrc, wv, (uint32_t)s * 128u + (uint32_t)(8 * pr + j) * (uint32_t)g.K,
+            kStreamed);
   };
 
   f32x4_t acc[NMB][4];
@@ -432,7 +433,13 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
   const uint32_t wbytes = (uint32_t)g.N * (uint32_t)g.K;
   const __amdgpu_buffer_rsrc_t wrsrc = raw_buffer(g.w + (int64_t)it.expert * wbytes, wbytes);
   const int64_t sat = (int64_t)it.expert * steps * KB + (cbase >> 7);
-  uint8_t* mine = ws + wave * 8192;
+  // four rows of 256 bytes at a time; slot s of row r holds chunk s ^ swz_t(r)
+  const int wrow = (wave >> 1) * 64 + (wave & 1) * 4 + (lane >> 4);
+  const int chunk = (lane & 15) ^ swz_t(wrow);
+  const uint32_t woff = (uint32_t)wrow * (uint32_t)g.K +
+                        (uint32_t)(min(it.nt * 256 + 64 * (chunk >> 2), g.K - 64) + 16 * (chunk & 3));
+  const int tr_row = 64 * (q & 1) + 32 * (q >> 1) + (i16 >> 1);
+  const int tr_at = tr_row * 256 + (((4 * wave) ^ swz_t(tr_row)) << 4) + (i16 & 1) * 8;
 
   f32x4_t acc[NMB][4];
 #pragma unroll
@@ -447,15 +454,11 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
       stage_w_scales<WF32>(g.w_scales, sat, KB, st, n, steps, wt);
     }
     rc.copy_part(st, g.N, wave, as);
-    // slot 4 r + s of a wavefront's 8 KiB holds chunk s ^ swz_t(r) of row r
+    // W rows past N lie past the buffer's end
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int slot = 64 * j + lane, r = slot >> 2;
-      const int chunk = (slot & 3) ^ swz_t(r);
-      const uint32_t n = st * 128 + r;
-      const uint32_t off = n < (uint32_t)g.N ? n * (uint32_t)g.K + cbase + 16 * chunk : 0xFFFFFFF0u;
-      copy16_to_lds(wrsrc, off, 0, mine + j * 1024);
-    }
+    for (int j = 0; j < 8; ++j)
+      copy16_to_lds<kStreamed>(wrsrc, woff + (uint32_t)(st * 128 + 8 * j) * (uint32_t)g.K, 0,
+                               ws + ((wave >> 1) * 64 + (wave & 1) * 4 + 8 * j) * 256);
     WStep w;
     __builtin_amdgcn_s_waitcnt(vm_lgkm0_imm(0));
     __syncthreads();
@@ -463,10 +466,8 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
     for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        // reduced values 64 (q & 1) + 32 (q / 2) + 8 t .. + 7, columns 16 nb ..
-        const int r = 64 * (q & 1) + 32 * (q >> 1) + 8 * t + (i16 >> 1);
-        const int slot = r * 4 + (nb ^ swz_t(r));
-        const i32x2_t v = lds_tr8(mine + slot * 16 + (i16 & 1) * 8);
+        // reduced values tr_row's eight + 8 t, columns 16 nb ..
+        const i32x2_t v = lds_tr8(ws + (tr_at ^ (nb << 4)) + t * 2048);
         w.w[nb][2 * t] = v[0];
         w.w[nb][2 * t + 1] = v[1];
       }
@@ -543,7 +544,7 @@ constexpr int kBigBlocks = 18;
 struct BigStage {
   uint8_t* a;                                    // [256][128]
   uint8_t* w;                                    // y = a W^T: [256 columns][128]
-};                                               // y = a W: [4 column groups][128][64]
+};                                               // y = a W: [128][256 columns]
 
 template <bool TRANS, bool WF32, int NMB>
 __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, const BigStage& s0,
@@ -573,10 +574,11 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
   const uint8_t* wbase = g.w + (int64_t)it.expert * wbytes;
   uint32_t woff;
   if constexpr (TRANS) {
-    // wavefront: 64 rows of one column group; slot 4 r + s holds chunk s ^ swz_t(r)
-    const int r = (wave & 1) * 64 + (lane >> 2);
-    const int c = min(it.nt * 256 + 64 * (wave >> 1), cols - 64);
-    woff = (uint32_t)r * (uint32_t)g.K + (uint32_t)(c + 16 * ((lane & 3) ^ swz_t(r)));
+    // four rows of 256 bytes at a time; slot s of row r holds chunk s ^ swz_t(r)
+    const int r = (wave >> 2) * 64 + (wave & 3) * 4 + (lane >> 4);
+    const int chunk = (lane & 15) ^ swz_t(r);
+    const int c = min(it.nt * 256 + 64 * (chunk >> 2), cols - 64);
+    woff = (uint32_t)r * (uint32_t)g.K + (uint32_t)(c + 16 * (chunk & 3));
   } else {
     woff = (uint32_t)(tid >> 3) * (uint32_t)g.K + (uint32_t)(((tid & 7) ^ swz_w(tid >> 3)) * 16);
   }
@@ -600,11 +602,11 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
     for (int i = 0; i < 4; ++i) {
       if constexpr (TRANS) {
         // W rows past N lie past the buffer's end
-        copy16_to_lds(rsrc, woff + (s0 * 128u + 16u * i) * (uint32_t)g.K, 0,
-                      s.w + (wave >> 1) * 8192 + (wave & 1) * 4096 + i * 1024);
+        copy16_to_lds<kStreamed>(rsrc, woff + (s0 * 128u + 16u * i) * (uint32_t)g.K, 0,
+                      s.w + ((wave >> 2) * 64 + (wave & 3) * 4 + 16 * i) * 256);
       } else {
         const uint32_t c = min(it.nt * 256 + 64 * i, cols - 64);
-        copy16_to_lds(rsrc, woff, c * (uint32_t)g.K + s0 * 128u,
+        copy16_to_lds<kStreamed>(rsrc, woff, c * (uint32_t)g.K + s0 * 128u,
                       s.w + (512 * i + 64 * wave) * 16);
       }
     }
@@ -619,7 +621,7 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
   const int at = rows_at(i16, q);
   const int ah = at + half * h0 * 2048;
   const int tr_row = 64 * (q & 1) + 32 * (q >> 1) + (i16 >> 1);
-  const int tr_at = nq * 8192 + tr_row * 64 + (swz_t(tr_row) << 4) + (i16 & 1) * 8;
+  const int tr_at = tr_row * 256 + (((4 * nq) ^ swz_t(tr_row)) << 4) + (i16 & 1) * 8;
 
   f32x4_t acc[NMB][4];
 #pragma unroll
@@ -630,10 +632,10 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
   auto read_w = [&](const BigStage& s, int nb, WStep& w) {
     if constexpr (TRANS) {
       // reduced values 64 (q & 1) + 32 (q / 2) + 8 t .. + 7, columns 16 nb ..:
-      // row r = tr_row + 8 t, chunk nb, whose slot is nb ^ swz_t(r)
+      // row r = tr_row + 8 t, chunk 4 nq + nb, whose slot differs by swz_t(r)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const i32x2_t v = lds_tr8(s.w + ((tr_at ^ (nb << 4)) + t * 512));
+        const i32x2_t v = lds_tr8(s.w + ((tr_at ^ (nb << 4)) + t * 2048));
         w.w[nb][2 * t] = v[0];
         w.w[nb][2 * t + 1] = v[1];
       }

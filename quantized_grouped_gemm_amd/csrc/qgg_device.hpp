@@ -182,16 +182,21 @@ __device__ __forceinline__ void wave_lds_sync() {
 // Compiler-only fence: no memory access moves across it; emits nothing.
 __device__ __forceinline__ void compiler_fence() { asm volatile("" ::: "memory"); }
 
+// Cache policy of a buffer access: the usual one, and that of data which is
+// read once (its lines are the first to leave the L2).
+constexpr int kCached = 0, kStreamed = 2;
+
 // 16 bytes from a buffer -> LDS without a register round trip
 // (buffer_load_dwordx4 ... lds): lane i of the wavefront writes lds + 16 i,
 // so the LDS pointer must be the same for the whole wavefront.  Offsets past
 // the buffer's size read zeros.  (The buffer form, unlike the global one, is
 // tracked by the compiler as an ordinary in-order vector-memory load, so its
 // own waits for register loads keep exact counts.)
+template <int CACHE = kCached>
 __device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff,
                                               uint32_t soff, void* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)lds, 16,
-                                           voff, soff, 0, 0);
+                                           voff, soff, 0, CACHE);
 }
 
 // Raw (untyped, unswizzled) buffer resource over [base, base + bytes).
