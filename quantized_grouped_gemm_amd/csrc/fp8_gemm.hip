@@ -85,10 +85,8 @@ __device__ __forceinline__ void find_item(int i, int ntn, const int* first, cons
   }
 }
 
-// Stages in the LDS ring of activation tiles, and weight steps in flight per
-// wavefront in registers (one step is 64 columns x 128 = 8 KiB).
+// Stages in the LDS ring of activation tiles.
 constexpr int kNBuf = 4;
-constexpr int kRing = 2;
 
 // One reduction step of a wavefront's 64 columns of W, as MFMA operands.
 struct WStep {
@@ -98,7 +96,7 @@ struct WStep {
 // The same as it is loaded.  Memory is read fastest where the four lanes of a
 // quad take 64 consecutive bytes, while an MFMA operand wants a lane to hold
 // one row: with one row a lane, every 16-byte piece is a cache access of its
-// own, and those bound the kernel (64 accesses a load, 84 % of all cycles).  So
+// own (64 a load, which took 84 % of the kernel's cycles).  So
 // lane 16 q + 4 a + p of load j of a pair of 16-row blocks (X, Y) takes chunk
 // p of half q & 1 of row 4 a + j of block q < 2 ? X : Y; a 4 x 4 transposition
 // in each quad gives the lane row 4 a + p's four chunks, and an exchange of
@@ -308,15 +306,20 @@ __device__ __forceinline__ void mfma_schedule() {
 
 // One item of y = a W^T: rows [row0, row0 + nrows) of an expert x 256
 // columns, NMB live 16-row blocks.  Weights go from memory straight into
-// registers, kRing steps ahead; the rows go through a ring of LDS stages,
-// kNBuf - 1 ahead; the barrier that ends a step waits for the next step's
-// copies only.  The loop is branch-free, four steps a round: past the last step
-// the weights repeat it and the rows are zeros with scale 1, which adds nothing.
+// registers, kRing steps ahead (a step of a wavefront is 64 columns x 128 = 8
+// KiB), past the caches, since one item uses them; the rows go through a ring of
+// LDS stages, kNBuf - 1 ahead; the barrier that ends a step waits for the next
+// step's copies only.  The loop is branch-free, in rounds of kRing steps: past
+// the last step the weights repeat it and the rows are zeros with scale 1, which
+// adds nothing.  Bound by the weights' bytes: 64 tokens over 384 uneven experts
+// of [4096][7168] take 218 us, 300 tokens over 64 experts 299 us, 6.3 TB/s of
+// the 6.3 that a plain stream of the same bytes reaches.
 template <bool WF32, int MB, int NMB>
 __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, const LdsRing4& As,
                                         uint8_t* sc, uint32_t* wt) {
   constexpr int kNCA = NMB / 2 > 0 ? NMB / 2 : 1;
   constexpr int kStageLoads = kNCA + 8;
+  constexpr int kRing = MB == 2 ? 4 : 2;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int i16 = lane & 15, q = lane >> 4;
@@ -380,15 +383,18 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
       mfma_step<WF32, NMB>(rows, w, ws, xs, at, acc);
       load_w(st0 + i + kRing, raw);
       mfma_schedule<WF32, NMB>();
-      // the copies of step i + 1 were issued two steps ago
-      stage_barrier<2 * kStageLoads>();
+      // the copies of step i + 1 were issued two steps ago, before weights
+      stage_barrier<2 * kStageLoads + 8>();
     };
     constexpr int kStage = 16 * MB * 128;
 #pragma nounroll
-    for (int i = 0; i < n; i += 2) {
-      const int odd = (i >> 1) & 1;
-      kstage(i, ring[0], As.b[0] + odd * kStage, As.b[1] + (odd ^ 1) * kStage);
-      kstage(i + 1, ring[1], As.b[1] + odd * kStage, As.b[0] + odd * kStage);
+    for (int i = 0; i < n; i += kRing) {
+#pragma unroll
+      for (int j = 0; j < kRing; j += 2) {
+        const int odd = ((i + j) >> 1) & 1;
+        kstage(i + j, ring[j], As.b[0] + odd * kStage, As.b[1] + (odd ^ 1) * kStage);
+        kstage(i + j + 1, ring[j + 1], As.b[1] + odd * kStage, As.b[0] + odd * kStage);
+      }
     }
     // the copies past the last step land, and every wavefront is done with the
     // ring and the scales, before they are written again
@@ -413,7 +419,10 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
 }
 
 // One item of y = a W: the weight step (128 rows of W x 64 columns a wavefront)
-// goes through LDS and comes back through transposing reads.
+// goes through LDS and comes back through transposing reads.  The copies take
+// whole lines: in pieces of 64 bytes, past the caches, a line is fetched twice.
+// Two workgroups a CU hide each other's waits; 64 tokens over 384 uneven experts
+// of [4096][7168] take 248 us, a seventh more than the other direction.
 template <bool WF32, int MB, int NMB>
 __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uint8_t* as,
                                        uint8_t* ws, uint8_t* sc, uint32_t* wt) {
@@ -490,9 +499,9 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
   }
 }
 
-// Workgroups take items (tile, 256 columns) in order, eight interleaved
-// stretches of them, one per XCD (workgroup b runs on XCD b mod 8): the columns
-// of a tile and the tiles of an expert then share one L2.
+// Workgroups take items (tile, 256 columns) in order, from eight stretches of
+// them, one per XCD (workgroup b runs on XCD b mod 8): the columns of a tile and
+// the tiles of an expert then share one L2.
 template <bool TRANS, bool WF32, int MB>
 __global__ __launch_bounds__(256, 2) void k_fp8_gemm(Fp8GemmArgs g, int ntn) {
   // separate objects: the compiler tells a copy into one from a read of another
@@ -536,10 +545,20 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm(Fp8GemmArgs g, int ntn) {
 }
 
 // ---- large tiles
-// 256 rows x 256 columns on eight wavefronts, two (halves of the rows) by four
-// (64 columns each).  Rows and weights both pass through LDS, two stages of 64
-// KiB: every byte that a workgroup asks its L2 for is used by 256 rows or
-// columns, which is what bounds a product of this size (see launch_sized).
+// 288 rows x 256 columns on eight wavefronts, two (halves of the rows) by four
+// (64 columns each): the most that the accumulators (144 registers a lane) and
+// two LDS stages of rows and weights (68 KiB each) leave room for.  A step's 36
+// matrix instructions on each of 8 wavefronts take 2304 cycles a CU, its LDS
+// reads (a row block by four wavefronts, a weight by two) and copies 2208 at 128
+// bytes a cycle, so neither waits long for the other; the rest of the time goes
+// into bringing 68 KiB a step to each CU.  8192 tokens, top-8 of 256 experts of
+// [4096][7168]: y = a W^T 1.88 ms (2.05 Pop/s), y = a W 2.11 ms (1.82 Pop/s);
+// without the copies 1.09 and 1.28 ms, with a quarter of the matrix instructions
+// 1.79 and 2.1 ms.  On the way here tiles of 256 rows, which half of these
+// experts exceed, took 2.38 ms against 2.18; a step that read its weights from
+// LDS at its start 2.18 and 2.57 against 2.08 and 2.26.  Weights go past the
+// caches: 7 % less time where an expert is one tile (its rows stay in L2), 0 to
+// 2 % more where several tiles share them.
 constexpr int kBigBlocks = 18;
 struct BigStage {
   uint8_t* a;                                    // [256][128]
@@ -806,30 +825,36 @@ __global__ __launch_bounds__(512, 1) void k_fp8_gemm_big(Fp8GemmArgs g, int ntn)
   }
 }
 
-// 16-row blocks per tile: an expert has at most one row per token, so small
-// batches fit every expert in one tile; larger ones go by the mean rows.
-int tile_blocks(const Fp8GemmArgs& g) {
-  const int64_t mean = (g.P + g.E - 1) / g.E;
-  const int64_t rows = std::min<int64_t>(g.T, 64) == g.T ? g.T : mean;
-  return rows <= 32 ? 2 : (rows <= 64 ? 4 : 8);
+// 16-row blocks per tile (an expert has at most one row per token, so up to 64
+// tokens every expert fits one tile of four).  Measured with weights [64][4096]
+// [7168], top-8, y = a W^T and y = a W, in us:
+//   mean rows             24         48         72        100
+//   four blocks     310 / 348  325 / 372  587 / 600  592 / 578
+//   eighteen        334 / 388  347 / 390  370 / 411  379 / 430
+// Two blocks leave registers for four steps of weights in flight instead of two.
+// That pays where the items do not fill the card (one token: 56 us against 66),
+// not beside another workgroup on the same CU (4 tokens 136 against 132, 16 tokens
+// 266 against 253).
+int tile_blocks(const Fp8GemmArgs& g, int ntn) {
+  if (!g.trans && g.T <= 32 && std::min<int64_t>(g.P, g.E) * ntn <= num_cus()) return 2;
+  return g.T <= 64 || (g.P + g.E - 1) / g.E <= 64 ? 4 : kBigBlocks;
 }
 
 }  // namespace
 
 template <bool TRANS, bool WF32>
 static void launch_sized(const Fp8GemmArgs& g, hipStream_t s) {
-  const int mb = tile_blocks(g);
-  const int mt = 16 * (mb == 8 ? kBigBlocks : mb);
-  const int64_t tiles = std::min<int64_t>(g.P, g.P / mt + g.E);
   const int ntn = ((TRANS ? g.K : g.N) + 255) / 256;
+  const int mb = tile_blocks(g, ntn);
+  const int64_t tiles = std::min<int64_t>(g.P, g.P / (16 * mb) + g.E);
   // a multiple of 8: one stretch of items per XCD
   const int64_t items = (tiles * ntn + 7) / 8 * 8, cus = num_cus() / 8 * 8;
-  const dim3 grid((unsigned)std::min<int64_t>(items, mb == 8 ? cus : 2 * cus));
-  if (mb == 8)
+  const dim3 grid((unsigned)std::min<int64_t>(items, mb == kBigBlocks ? cus : 2 * cus));
+  if (mb == kBigBlocks)
     hipLaunchKernelGGL((k_fp8_gemm_big<TRANS, WF32>), grid, dim3(512), 0, s, g, ntn);
   else if (mb == 4)
     hipLaunchKernelGGL((k_fp8_gemm<TRANS, WF32, 4>), grid, dim3(256), 0, s, g, ntn);
-  else
+  else if constexpr (!TRANS)
     hipLaunchKernelGGL((k_fp8_gemm<TRANS, WF32, 2>), grid, dim3(256), 0, s, g, ntn);
 }
 
