@@ -75,8 +75,9 @@ __device__ __forceinline__ void find_item(int i, int ntn, const int* first, cons
     const int p = i - f * ntn;
     if (p >= 0 && p < n * ntn) {
       const int nt = p / n, k = p - nt * n;
-      const int c = counts[e], blocks = (c + 15) >> 4;     // split into equal numbers of blocks
-      const int b0 = k * blocks / n, b1 = (k + 1) * blocks / n;
+      const int c = counts[e];
+      const int64_t blocks = (c + 15) >> 4;      // split into equal numbers of blocks
+      const int b0 = (int)(k * blocks / n), b1 = (int)((k + 1) * blocks / n);
       out[0] = e;
       out[1] = offsets[e] + 16 * b0;
       out[2] = min(16 * b1, c) - 16 * b0;
@@ -312,7 +313,7 @@ __device__ __forceinline__ void mfma_schedule() {
 // step's copies only.  The loop is branch-free, in rounds of kRing steps: past
 // the last step the weights repeat it and the rows are zeros with scale 1, which
 // adds nothing.  Bound by the weights' bytes: 64 tokens over 384 uneven experts
-// of [4096][7168] take 218 us, 300 tokens over 64 experts 299 us, 6.3 TB/s of
+// of [4096][7168] take 217 us, 300 tokens over 64 experts 299 us, 6.3 TB/s of
 // the 6.3 that a plain stream of the same bytes reaches.
 template <bool WF32, int MB, int NMB>
 __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, const LdsRing4& As,
@@ -360,17 +361,16 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
     WRaw ring[kRing];
     rc.copy_whole(st0, steps, wave, As.b[0]);
     rc.copy_whole(st0 + 1, steps, wave, As.b[1]);
-    rc.copy_whole(st0 + 2, steps, wave, As.b[0] + 16 * MB * 128);
+    rc.copy_whole(st0 + 2, steps, wave, As.b[2]);
     compiler_fence();
 #pragma unroll
     for (int r = 0; r < kRing; ++r) load_w(st0 + r, ring[r]);
     stage_scales<MB, NMB>(g, it, st0, n, steps, sc);
     stage_w_scales<WF32>(g.w_scales, sat, 1, st0, n, steps, wt);
     stage_barrier<0>();
-    // step i reads stage (i / 2) & 1 of object i & 1 while step i + 3 goes to
-    // the other object
     auto kstage = [&](int i, WRaw& raw, const uint8_t* rows, uint8_t* next) {
       rc.copy_whole(st0 + i + kNBuf - 1, steps, wave, next);
+      compiler_fence();                          // the wait below counts on this order
       const int xs = read_scales<MB>(sc, i, i16);
       const uint32_t ws = wt[wave * kPiece + i];
       WStep w;
@@ -386,16 +386,11 @@ __device__ __forceinline__ void nt_item(const Fp8GemmArgs& g, const Item& it, co
       // the copies of step i + 1 were issued two steps ago, before weights
       stage_barrier<2 * kStageLoads + 8>();
     };
-    constexpr int kStage = 16 * MB * 128;
 #pragma nounroll
-    for (int i = 0; i < n; i += kRing) {
+    for (int i = 0; i < n; i += kNBuf)
 #pragma unroll
-      for (int j = 0; j < kRing; j += 2) {
-        const int odd = ((i + j) >> 1) & 1;
-        kstage(i + j, ring[j], As.b[0] + odd * kStage, As.b[1] + (odd ^ 1) * kStage);
-        kstage(i + j + 1, ring[j + 1], As.b[1] + odd * kStage, As.b[0] + odd * kStage);
-      }
-    }
+      for (int j = 0; j < kNBuf; ++j)
+        kstage(i + j, ring[j % kRing], As.b[j], As.b[(j + kNBuf - 1) % kNBuf]);
     // the copies past the last step land, and every wavefront is done with the
     // ring and the scales, before they are written again
     __builtin_amdgcn_s_waitcnt(vm_lgkm0_imm(0));
@@ -505,10 +500,13 @@ __device__ __forceinline__ void t_item(const Fp8GemmArgs& g, const Item& it, uin
 template <bool TRANS, bool WF32, int MB>
 __global__ __launch_bounds__(256, 2) void k_fp8_gemm(Fp8GemmArgs g, int ntn) {
   // separate objects: the compiler tells a copy into one from a read of another
-  __shared__ __attribute__((aligned(16))) uint8_t b0[16 * MB * 256];
-  __shared__ __attribute__((aligned(16))) uint8_t b1[TRANS ? 32768 : 16 * MB * 256];
+  constexpr int kRows = 16 * MB * 128;
+  __shared__ __attribute__((aligned(16))) uint8_t b0[kRows];
+  __shared__ __attribute__((aligned(16))) uint8_t b1[TRANS ? 32768 : kRows];
+  __shared__ __attribute__((aligned(16))) uint8_t b2[TRANS ? 16 : kRows];
+  __shared__ __attribute__((aligned(16))) uint8_t b3[TRANS ? 16 : kRows];
   __shared__ __attribute__((aligned(16))) uint8_t sc[kPiece * 16 * MB];
-  const LdsRing4 As{{b0, b1, nullptr, nullptr}};
+  const LdsRing4 As{{b0, b1, b2, b3}};
   __shared__ int scratch[16];
   __shared__ int item[4];
   __shared__ uint32_t wt[4 * kPiece];
@@ -677,7 +675,9 @@ __device__ __forceinline__ void big_item(const Fp8GemmArgs& g, const Item& it, c
   WStep w;
   auto step = [&](int st0, int i, int n, const BigStage& s, const BigStage& t) {
     copy_a(st0 + i + 1, i + 1 < n, t);
+    compiler_fence();                            // the waits below count on this order
     copy_w(st0 + i + 2, i + 2 < n, s);
+    compiler_fence();
     int xs[3];
     const uint2 v = *reinterpret_cast<const uint2*>(sc + ((i * 2 + half) * 16 + i16) * 8);
     xs[0] = (int)v.x;
@@ -832,7 +832,7 @@ __global__ __launch_bounds__(512, 1) void k_fp8_gemm_big(Fp8GemmArgs g, int ntn)
 //   four blocks     310 / 348  325 / 372  587 / 600  592 / 578
 //   eighteen        334 / 388  347 / 390  370 / 411  379 / 430
 // Two blocks leave registers for four steps of weights in flight instead of two.
-// That pays where the items do not fill the card (one token: 56 us against 66),
+// That pays where the items do not fill the card (one token: 55 us against 66),
 // not beside another workgroup on the same CU (4 tokens 136 against 132, 16 tokens
 // 266 against 253).
 int tile_blocks(const Fp8GemmArgs& g, int ntn) {

@@ -691,6 +691,24 @@ def test_fp8_grouped_gemm_long_rows():
         check_gemm(w, rows, p, T, k, f, qgg.fp8_grouped_gemm(w, *rows, p, T, k, flags=f))
 
 
+def test_fp8_grouped_gemm_millions_of_rows_of_one_expert():
+    # the tiles' shares of the row blocks pass 32 bits
+    T, N, K = 4_000_003, 64, 128
+    g = gen(77)
+    w = weights(g, 1, N, K, False)
+    p = perm_of(torch.zeros((T, 1), dtype=torch.int32), 1)
+    few = normal(g, 4099, K).to(DEV)
+    codes, scales = qgg.fp8_quantize(few)
+    source = torch.arange(T, device=DEV) % len(few)
+    a = codes.view(torch.uint8)[source].contiguous()
+    y = qgg.fp8_grouped_gemm(w, a, scales.view(torch.uint8)[source].contiguous(), p, T, 1)
+    small = perm_of(torch.zeros((len(few), 1), dtype=torch.int32), 1)
+    one = qgg.fp8_grouped_gemm(w, codes, scales, small, len(few), 1)
+    check_gemm(w, (codes, scales), small, len(few), 1, qgg.A_TOKENS, one)
+    # a row's result does not hang on the rows beside it
+    assert torch.equal(y, one[source[p.perm.long()]])
+
+
 def test_empty_batches():
     g = gen(1)
     w = weights(g, 4, 128, 256, False)
