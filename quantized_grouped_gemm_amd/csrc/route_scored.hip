@@ -386,6 +386,10 @@ __device__ __forceinline__ int choose32(const float (&l)[NV], const float* bias,
 }
 
 // One wavefront per token; lane l holds experts l, l + 64, ... (NV of them).
+// Bound by latency: k dependent rounds of a reduction over the lanes.  64 tokens,
+// 384 experts, softmax: 6.5 us against 9.2 with 64-bit keys through LDS permutes;
+// 8192 tokens, 256 experts in 8 groups, sigmoid: 18 us, where 8.9 MB are the
+// bytes of 2 us.
 template <int NV, typename L>
 __global__ __launch_bounds__(256) void k_route_scored(const L* __restrict__ logits,
                                                       const float* __restrict__ bias, int T, int E,
