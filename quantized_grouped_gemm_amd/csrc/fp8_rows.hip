@@ -155,8 +155,12 @@ __device__ __forceinline__ float pick(const float v[8], int i) {
 // on the order of the operations before it, and two programs, or a 64-bit
 // reference, have the same.  kMargin bounds the relative width of an interval
 // around a block's maximum: within it of a border of scales (or with values
-// that are not finite) the whole block is taken exactly.
+// that are not finite) the whole block is taken exactly.  So is a block of
+// values below kTiny, where a product on the way to one may have left the
+// normal numbers and lost more than its interval allows; above kTiny that would
+// take factors past 2^50 after such a product.
 constexpr float kMargin = 0x1p-15f;
+constexpr uint32_t kTiny = 67u << 23;            // 2^-60
 
 // HI: |hi| >= |lo|.  `all`: a lane has a value that lo and hi do not hold.
 template <bool HI, typename Exact>
@@ -171,7 +175,8 @@ __device__ __forceinline__ uint2 quantize8_exact(const float lo[8], const float 
   top = row16_max(top);
   *code = block_scale(top);
   const float low = __uint_as_float(top) * (1.0f - kMargin);
-  if (__any(all || top >= kInfBits || block_scale(mag_bits(low)) != *code)) {
+  if (__any(all || (top != 0 && top < kTiny) || top >= kInfBits ||
+            block_scale(mag_bits(low)) != *code)) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = exact(i);

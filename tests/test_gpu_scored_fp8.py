@@ -488,6 +488,22 @@ def test_swiglu_fp8_bwd(T, k, inter, drop):
         assert r["dgates"][0, 0] == 0 and r["dgates"][-1, -1] == 0
 
 
+@pytest.mark.parametrize("down", [-20, -30, -34, -40, -46])
+def test_swiglu_fp8_bwd_of_tiny_gradients(down):
+    # gates times da below the normal numbers of 32 bits
+    g = gen(40 - down)
+    T, k, I = 16, 2, 512
+    p = perm_of(torch.tensor([[0, 1]] * T, dtype=torch.int32), 2)
+    h = normal(g, T * k, 2 * I, std=2.0)
+    h[:, I:] *= 2.0 ** 12
+    h8, hs = qgg.fp8_quantize(h.to(DEV))
+    da = normal(g, T * k, I) * 2.0 ** down
+    gates = (torch.rand(T, k, generator=g) + 0.5) * 2.0 ** -100
+    r = qgg.swiglu_fp8_bwd(da.to(DEV), h8, hs, gates.to(DEV), p, want=("dh8",))
+    dh = swiglu_bwd64(da, value(h8, hs), gates, p.perm.cpu().numpy(), T * k)[0]
+    check_exact((r["dh8"], r["dh8_scales"]), dh)
+
+
 def test_swiglu_gradient_by_differences():
     g = gen(3)
     T, k, I = 2, 2, 128
